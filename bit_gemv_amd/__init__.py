@@ -18,6 +18,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "librfp2.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "rfp2.h")
 
+KV_F16, KV_I8 = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ATTN_MAX_NEW = 8
+
 RFP2_OK, RFP2_E_NULL, RFP2_E_SHAPE, RFP2_E_ALIGN, RFP2_E_LAUNCH = 0, -1, -2, -3, -4
 GEMV_MAX_M = 8
 
@@ -25,6 +29,18 @@ _lib = None
 
 _c_i64 = ctypes.c_int64
 _c_p = ctypes.c_void_p
+_c_f64 = ctypes.c_double
+
+
+class _KvCacheStruct(ctypes.Structure):
+    """rfp2_kv_cache of include/rfp2.h."""
+    _fields_ = [("k", _c_p), ("v", _c_p), ("k_scale", _c_p), ("v_scale", _c_p),
+                ("page_table", _c_p), ("seqs", _c_i64), ("max_pages", _c_i64),
+                ("pages", _c_i64), ("page_size", _c_i64), ("kv_heads", _c_i64),
+                ("head_dim", _c_i64), ("format", ctypes.c_int32)]
+
+
+_c_cache = ctypes.POINTER(_KvCacheStruct)
 _SIGNATURES = {
     "rfp2_abi_version": ([], ctypes.c_int),
     "rfp2_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -44,6 +60,20 @@ _SIGNATURES = {
                        _c_p, _c_p, ctypes.c_size_t, _c_p], ctypes.c_int),
     "rfp2_moe_gemm_noalloc": ([_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p,
                                _c_p, _c_p, _c_p], ctypes.c_int),
+    "rfp2_rope_freqs": ([_c_i64, _c_f64, _c_f64, _c_f64, _c_f64, _c_f64, _c_p, _c_p],
+                        ctypes.c_int),
+    "rfp2_rope": ([_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i64, ctypes.c_int,
+                   _c_f64, _c_p, _c_i64, _c_p], ctypes.c_int),
+    "rfp2_kv_write": ([_c_cache, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p],
+                      ctypes.c_int),
+    "rfp2_rope_kv_write": ([_c_cache, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64,
+                            _c_p, _c_p, _c_p, _c_i64, ctypes.c_int, _c_f64, _c_p, _c_i64, _c_p,
+                            _c_p], ctypes.c_int),
+    "rfp2_kv_read": ([_c_cache, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p],
+                     ctypes.c_int),
+    "rfp2_paged_attn_workspace_bytes": ([_c_cache, _c_i64, _c_i64, _c_i64], ctypes.c_size_t),
+    "rfp2_paged_attn": ([_c_cache, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, ctypes.c_float,
+                         _c_i64, _c_p, _c_p, _c_p, ctypes.c_size_t, _c_p], ctypes.c_int),
     "rfp2_read_ceiling": ([_c_p, _c_i64, ctypes.c_uint32, _c_p, _c_p], ctypes.c_int),
     "rfp2_quant_gemv": ([_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p], ctypes.c_int),
     "rfp2_quant_moe_gemv": ([_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p,
@@ -280,6 +310,192 @@ def rfp2_quant_moe_gemv(w, E: int, N: int, K: int, ids, top_k: int, a, q, d, y, 
         _ptr(a, torch.float32, K, "a"), _ptr(q, torch.int8, K, "q"),
         _ptr(d, torch.float32, _blocks(K), "d"),
         _ptr(y, torch.float32, top_k * N, "y"), errp, _stream(stream)))
+
+
+class KvCache:
+    """The rfp2_kv_cache of a set of tensors (kept alive by this object):
+
+      k [pages, kv_heads, page_size, head_dim] and v [pages, kv_heads,
+      page_size/8, head_dim, 8], both float16 (KV_F16) or int8 (KV_I8);
+      k_scale, v_scale [pages, kv_heads, page_size/8, head_dim/32, 8] float32
+      for int8, None for float16; page_table [seqs, max_pages] int32.
+
+    All contiguous, on one GPU.  The tensors' contents may change between
+    calls (the page table's too); their shapes are checked here, once."""
+
+    def __init__(self, k, v, k_scale, v_scale, page_table):
+        import torch
+        if not isinstance(k, torch.Tensor) or k.dtype not in (torch.float16, torch.int8):
+            raise TypeError("k must be a float16 or int8 torch tensor")
+        if k.dim() != 4:
+            raise ValueError("k must be [pages, kv_heads, page_size, head_dim]")
+        pages, heads, size, dim = k.shape
+        i8 = k.dtype == torch.int8
+        if size % 8 or dim % 32:
+            raise ValueError("page_size must be a multiple of 8 and head_dim of 32")
+
+        def check(t, dtype, shape, name):
+            p = _ptr(t, dtype, 0, name)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
+            if t.device != k.device:
+                raise ValueError(f"{name} must be on {k.device} like k (got {t.device})")
+            return p
+
+        scale_shape = (pages, heads, size // 8, dim // 32, 8)
+        kp = check(k, k.dtype, (pages, heads, size, dim), "k")
+        vp = check(v, k.dtype, (pages, heads, size // 8, dim, 8), "v")
+        if i8:
+            ksp = check(k_scale, torch.float32, scale_shape, "k_scale")
+            vsp = check(v_scale, torch.float32, scale_shape, "v_scale")
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a float16 cache has no scales")
+        else:
+            ksp = vsp = None
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table must be a [seqs, max_pages] torch tensor")
+        tp = check(page_table, torch.int32, tuple(page_table.shape), "page_table")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_table = page_table
+        self.device, self.kv_heads, self.head_dim = k.device, heads, dim
+        self.seqs, self.page_size = page_table.shape[0], size
+        self.format = KV_I8 if i8 else KV_F16
+        self._struct = _KvCacheStruct(kp, vp, ksp, vsp, tp, page_table.shape[0],
+                                      page_table.shape[1], pages, size, heads, dim, self.format)
+
+    @classmethod
+    def allocate(cls, format: int, pages: int, page_size: int, kv_heads: int, head_dim: int,
+                 page_table):
+        """A cache of new, zeroed memory (on the page table's GPU) behind a page table."""
+        import torch
+        if format not in (KV_F16, KV_I8):
+            raise ValueError("format must be KV_F16 or KV_I8")
+        dt = torch.int8 if format == KV_I8 else torch.float16
+
+        def zeros(*shape, dtype=dt):
+            return torch.zeros(shape, dtype=dtype, device=page_table.device)
+
+        s = [zeros(pages, kv_heads, page_size // 8, head_dim // 32, 8, dtype=torch.float32)
+             for _ in range(2)] if format == KV_I8 else [None, None]
+        return cls(zeros(pages, kv_heads, page_size, head_dim),
+                   zeros(pages, kv_heads, page_size // 8, head_dim, 8), *s, page_table)
+
+
+def _cache_ref(cache):
+    if not isinstance(cache, KvCache):
+        raise TypeError("cache must be a KvCache")
+    return ctypes.byref(cache._struct)
+
+
+def _rows(t, T: int, width: int, name: str):
+    """(device pointer, elements between rows) of a float32 tensor whose first
+    dimension counts T or more rows of `width` or more values, contiguous in a
+    row (so a slice of a product's columns will do)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU (got {t.device})")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32 (got {t.dtype})")
+    if t.dim() < 2 or t.shape[0] < T:
+        raise ValueError(f"{name} must have {T} or more rows (shape {tuple(t.shape)})")
+    row = t[0]
+    if not row.is_contiguous() or row.numel() < width:
+        raise ValueError(f"a row of {name} must be {width} or more contiguous values")
+    stride = t.stride(0)
+    return t.data_ptr(), stride if T > 1 else max(stride, width)
+
+
+def rfp2_rope_freqs(rot: int, base: float, factor: float, orig_len: float, low_turns: float,
+                    high_turns: float, freqs, stream=None) -> None:
+    import torch
+    _check("rfp2_rope_freqs", lib().rfp2_rope_freqs(
+        rot, base, factor, orig_len, low_turns, high_turns,
+        _ptr(freqs, torch.float64, rot // 2, "freqs"), _stream(stream)))
+
+
+def rfp2_rope(x, T: int, H: int, D: int, pos, freqs, rot: int, style: int, mscale: float, y,
+              stream=None) -> None:
+    """x, y: T rows of H * D values ([T, H, D] or [T, H * D]); rows may lie
+    apart.  y may be x."""
+    import torch
+    xp, xs = _rows(x, T, H * D, "x")
+    yp, ys = _rows(y, T, H * D, "y")
+    _check("rfp2_rope", lib().rfp2_rope(
+        xp, T, H, D, xs, _ptr(pos, torch.int32, T, "pos"),
+        _ptr(freqs, torch.float64, rot // 2, "freqs"), rot, style, mscale, yp, ys,
+        _stream(stream)))
+
+
+def rfp2_kv_write(cache, k, v, T: int, seq, pos, err=None, stream=None) -> None:
+    import torch
+    row = cache.kv_heads * cache.head_dim
+    kp, ks = _rows(k, T, row, "k")
+    vp, vs = _rows(v, T, row, "v")
+    errp = None if err is None else _ptr(err, torch.int32, 1, "err")
+    _check("rfp2_kv_write", lib().rfp2_kv_write(
+        _cache_ref(cache), kp, vp, T, ks, vs, _ptr(seq, torch.int32, T, "seq"),
+        _ptr(pos, torch.int32, T, "pos"), errp, _stream(stream)))
+
+
+def rfp2_rope_kv_write(cache, q, k, v, T: int, H: int, seq, pos, freqs, rot: int, style: int,
+                       mscale: float, q_out, err=None, stream=None) -> None:
+    """q, q_out: T rows of H heads (both None with H == 0: keys alone)."""
+    import torch
+    row = cache.kv_heads * cache.head_dim
+    qp, qs, op, os_ = None, 0, None, 0
+    if H:
+        qp, qs = _rows(q, T, H * cache.head_dim, "q")
+        op, os_ = _rows(q_out, T, H * cache.head_dim, "q_out")
+    kp, ks = _rows(k, T, row, "k")
+    vp, vs = _rows(v, T, row, "v")
+    errp = None if err is None else _ptr(err, torch.int32, 1, "err")
+    _check("rfp2_rope_kv_write", lib().rfp2_rope_kv_write(
+        _cache_ref(cache), qp, kp, vp, T, H, qs, ks, vs, _ptr(seq, torch.int32, T, "seq"),
+        _ptr(pos, torch.int32, T, "pos"), _ptr(freqs, torch.float64, rot // 2, "freqs"), rot,
+        style, mscale, op, os_, errp, _stream(stream)))
+
+
+def rfp2_kv_read(cache, T: int, seq, pos, k, v, err=None, stream=None) -> None:
+    import torch
+    row = cache.kv_heads * cache.head_dim
+    kp, ks = _rows(k, T, row, "k")
+    vp, vs = _rows(v, T, row, "v")
+    errp = None if err is None else _ptr(err, torch.int32, 1, "err")
+    _check("rfp2_kv_read", lib().rfp2_kv_read(
+        _cache_ref(cache), T, _ptr(seq, torch.int32, T, "seq"),
+        _ptr(pos, torch.int32, T, "pos"), kp, vp, ks, vs, errp, _stream(stream)))
+
+
+def rfp2_paged_attn_workspace_bytes(cache, B: int, new_tokens: int, H: int) -> int:
+    return int(lib().rfp2_paged_attn_workspace_bytes(_cache_ref(cache), B, new_tokens, H))
+
+
+def rfp2_paged_attn(cache, q, B: int, new_tokens: int, H: int, lens, scale: float, y,
+                    window: int = 0, err=None, workspace=None, stream=None) -> None:
+    """q: [B, new_tokens, ...] or [B * new_tokens, ...], H * D contiguous values
+    a row, the rows evenly spaced; y: [B, new_tokens, H, D], contiguous.
+    workspace: a uint8 GPU tensor of at least rfp2_paged_attn_workspace_bytes
+    bytes; when None, one is allocated for this call (on the current stream
+    only: a call on another stream brings its own)."""
+    import torch
+    rows, width = B * new_tokens, H * cache.head_dim
+    if isinstance(q, torch.Tensor) and q.dim() > 2 and q.shape[0] == B and q.shape[1] == new_tokens:
+        if B > 1 and new_tokens > 1 and q.stride(0) != new_tokens * q.stride(1):
+            raise ValueError("the rows of q must be evenly spaced")
+        q = q[:, 0] if new_tokens == 1 else q[0] if B == 1 else q.view(rows, *q.shape[2:])
+    qp, qs = _rows(q, rows, width, "q")
+    if workspace is None:
+        if stream is not None:
+            raise ValueError("a call on a stream of its own needs a workspace")
+        need = rfp2_paged_attn_workspace_bytes(cache, B, new_tokens, H)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=y.device)
+    errp = None if err is None else _ptr(err, torch.int32, 1, "err")
+    _check("rfp2_paged_attn", lib().rfp2_paged_attn(
+        _cache_ref(cache), qp, B, new_tokens, H, qs, _ptr(lens, torch.int32, B, "lens"), scale,
+        window, _ptr(y, torch.float32, rows * width, "y"), errp,
+        _ptr(workspace, torch.uint8, 0, "workspace"), workspace.numel(), _stream(stream)))
 
 
 def rfp2_debug_decode(w, N: int, K: int, codes_out, scales_out, stream=None) -> None:

@@ -1,6 +1,8 @@
 // C ABI of the library (declared in include/rfp2.h).  Every entry point checks
 // its arguments on the host and returns a status before anything is enqueued;
 // no HIP call is made for a rejected call.
+#include <cmath>
+
 #include "rfp2.h"
 #include "rfp2_internal.h"
 
@@ -8,6 +10,7 @@ namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;     // row and token counts
 constexpr int64_t kMaxGemvK = 32768;               // staged activations fit LDS
+constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;  // pages and cached positions
 constexpr int64_t kMaxSortSlots = int64_t(1) << 24;  // routed slots of one sort
 
 bool aligned(const void* p, uintptr_t a) {
@@ -20,6 +23,56 @@ rfp2_status from_hip(hipError_t e) {
 
 bool product_k_ok(int64_t K) {
   return K >= 256 && K % 256 == 0 && K <= kMaxGemvK;
+}
+
+// A cache descriptor with everything the kernels index by in range; RFP2_OK and
+// the kernels' view of it, or the status to return.
+rfp2_status check_cache(const rfp2_kv_cache* c, rfp2::KvView* view) {
+  if (!c) return RFP2_E_NULL;
+  const bool i8 = c->format == RFP2_KV_I8;
+  if (!i8 && c->format != RFP2_KV_F16) return RFP2_E_SHAPE;
+  if (!c->k || !c->v || !c->page_table || (i8 && (!c->k_scale || !c->v_scale)))
+    return RFP2_E_NULL;
+  const int64_t P = c->page_size;
+  if (c->kv_heads < 1 || c->kv_heads > 1024 || c->head_dim < 32 || c->head_dim > 256 ||
+      c->head_dim % 32 != 0 || P < 8 || P > 4096 || (P & (P - 1)) != 0 || c->pages < 1 ||
+      c->pages > kMaxIndex || c->seqs < 1 || c->seqs > (int64_t(1) << 20) || c->max_pages < 1 ||
+      c->max_pages > kMaxIndex / P)
+    return RFP2_E_SHAPE;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4) ||
+      (i8 && (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))))
+    return RFP2_E_ALIGN;
+  int shift = 3;
+  while ((int64_t(1) << shift) < P) ++shift;
+  *view = {c->k, c->v, i8 ? c->k_scale : nullptr, i8 ? c->v_scale : nullptr, c->page_table,
+           (int32_t)c->seqs, (int32_t)c->max_pages, (int32_t)c->pages, shift,
+           (int32_t)c->kv_heads, (int32_t)c->head_dim};
+  return RFP2_OK;
+}
+
+// Rows of `need` fp32 values that lie `stride` apart and are read 16 bytes at
+// a time.
+bool row_stride_ok(int64_t stride, int64_t need) {
+  return stride >= need && stride % 4 == 0 && stride <= (int64_t(1) << 40);
+}
+
+bool rope_ok(int64_t rot, int64_t D, int style, double mscale) {
+  return rot >= 2 && rot <= D && rot % 2 == 0 &&
+         (style == RFP2_ROPE_HALF || style == RFP2_ROPE_INTERLEAVED) && std::isfinite(mscale);
+}
+
+// The checks that writing and reading T tokens share.
+rfp2_status check_kv_rows(const rfp2::KvView& c, const void* k, const void* v, int64_t T,
+                          int64_t k_stride, int64_t v_stride, const int32_t* seq,
+                          const int32_t* pos, const int32_t* err) {
+  if (!k || !v || !seq || !pos) return RFP2_E_NULL;
+  const int64_t row = (int64_t)c.heads * c.dim;
+  if (T < 1 || T > kMaxRows || !row_stride_ok(k_stride, row) || !row_stride_ok(v_stride, row))
+    return RFP2_E_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(seq, 4) || !aligned(pos, 4) ||
+      (err && !aligned(err, 4)))
+    return RFP2_E_ALIGN;
+  return RFP2_OK;
 }
 
 }  // namespace
@@ -196,6 +249,119 @@ rfp2_status rfp2_moe_gemm_noalloc(const uint8_t* w, int64_t E, int64_t N, int64_
   (void)hipGetLastError();
   return from_hip(
       rfp2::launch_moe_gemm_noalloc(w, E, N, K, ids, T, top_k, q, d, y, err, stream));
+}
+
+rfp2_status rfp2_rope_freqs(int64_t rot, double base, double factor, double orig_len,
+                            double low_turns, double high_turns, double* freqs,
+                            hipStream_t stream) {
+  if (!freqs) return RFP2_E_NULL;
+  if (rot < 2 || rot > rfp2::kMaxRopeDim || rot % 2 != 0 || !std::isfinite(base) ||
+      !(base > 1.0) || !std::isfinite(factor) || !(factor >= 1.0) || !std::isfinite(orig_len) ||
+      !(orig_len >= 0.0))
+    return RFP2_E_SHAPE;
+  if (orig_len > 0.0 && (!std::isfinite(high_turns) || !(low_turns >= 0.0) ||
+                         !(low_turns < high_turns)))
+    return RFP2_E_SHAPE;
+  if (!aligned(freqs, 8)) return RFP2_E_ALIGN;
+  (void)hipGetLastError();
+  return from_hip(rfp2::launch_rope_freqs(rot, base, factor, orig_len, low_turns, high_turns,
+                                          freqs, stream));
+}
+
+rfp2_status rfp2_rope(const float* x, int64_t T, int64_t H, int64_t D, int64_t x_stride,
+                      const int32_t* pos, const double* freqs, int64_t rot, int style,
+                      double mscale, float* y, int64_t y_stride, hipStream_t stream) {
+  if (!x || !pos || !freqs || !y) return RFP2_E_NULL;
+  if (T < 1 || T > kMaxRows || H < 1 || D < 4 || D > rfp2::kMaxRopeDim || D % 4 != 0 ||
+      H > (int64_t(1) << 24) / D || !row_stride_ok(x_stride, H * D) ||
+      !row_stride_ok(y_stride, H * D) || (x == y && x_stride != y_stride) ||
+      !rope_ok(rot, D, style, mscale))
+    return RFP2_E_SHAPE;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(pos, 4) || !aligned(freqs, 8))
+    return RFP2_E_ALIGN;
+  (void)hipGetLastError();
+  const rfp2::RopeView rope = {freqs, mscale, (int32_t)rot, style == RFP2_ROPE_INTERLEAVED};
+  return from_hip(rfp2::launch_rope(x, T, H, D, x_stride, pos, rope, y, y_stride, stream));
+}
+
+rfp2_status rfp2_kv_write(const rfp2_kv_cache* cache, const float* k, const float* v, int64_t T,
+                          int64_t k_stride, int64_t v_stride, const int32_t* seq,
+                          const int32_t* pos, int32_t* err, hipStream_t stream) {
+  rfp2::KvView c;
+  rfp2_status st = check_cache(cache, &c);
+  if (st == RFP2_OK) st = check_kv_rows(c, k, v, T, k_stride, v_stride, seq, pos, err);
+  if (st != RFP2_OK) return st;
+  (void)hipGetLastError();
+  const rfp2::RopeView none = {nullptr, 1.0, 0, 0};
+  return from_hip(rfp2::launch_kv_write(c, cache->format == RFP2_KV_I8, nullptr, k, v, T, 0, 0,
+                                        k_stride, v_stride, seq, pos, none, nullptr, 0, err,
+                                        stream));
+}
+
+rfp2_status rfp2_rope_kv_write(const rfp2_kv_cache* cache, const float* q, const float* k,
+                               const float* v, int64_t T, int64_t H, int64_t q_stride,
+                               int64_t k_stride, int64_t v_stride, const int32_t* seq,
+                               const int32_t* pos, const double* freqs, int64_t rot, int style,
+                               double mscale, float* q_out, int64_t q_out_stride, int32_t* err,
+                               hipStream_t stream) {
+  rfp2::KvView c;
+  rfp2_status st = check_cache(cache, &c);
+  if (st == RFP2_OK) st = check_kv_rows(c, k, v, T, k_stride, v_stride, seq, pos, err);
+  if (st != RFP2_OK) return st;
+  if (!freqs || (H != 0 && (!q || !q_out))) return RFP2_E_NULL;
+  if (H < 0 || H > (int64_t(1) << 24) / c.dim || !rope_ok(rot, c.dim, style, mscale))
+    return RFP2_E_SHAPE;
+  if (H > 0 && (!row_stride_ok(q_stride, H * c.dim) || !row_stride_ok(q_out_stride, H * c.dim)))
+    return RFP2_E_SHAPE;
+  if (!aligned(freqs, 8) || !aligned(q, 16) || !aligned(q_out, 16)) return RFP2_E_ALIGN;
+  (void)hipGetLastError();
+  const rfp2::RopeView rope = {freqs, mscale, (int32_t)rot, style == RFP2_ROPE_INTERLEAVED};
+  return from_hip(rfp2::launch_kv_write(c, cache->format == RFP2_KV_I8, q, k, v, T, H, q_stride,
+                                        k_stride, v_stride, seq, pos, rope, q_out, q_out_stride,
+                                        err, stream));
+}
+
+rfp2_status rfp2_kv_read(const rfp2_kv_cache* cache, int64_t T, const int32_t* seq,
+                         const int32_t* pos, float* k, float* v, int64_t k_stride,
+                         int64_t v_stride, int32_t* err, hipStream_t stream) {
+  rfp2::KvView c;
+  rfp2_status st = check_cache(cache, &c);
+  if (st == RFP2_OK) st = check_kv_rows(c, k, v, T, k_stride, v_stride, seq, pos, err);
+  if (st != RFP2_OK) return st;
+  (void)hipGetLastError();
+  return from_hip(rfp2::launch_kv_read(c, cache->format == RFP2_KV_I8, T, seq, pos, k, v,
+                                       k_stride, v_stride, err, stream));
+}
+
+size_t rfp2_paged_attn_workspace_bytes(const rfp2_kv_cache* cache, int64_t B, int64_t new_tokens,
+                                       int64_t H) {
+  rfp2::KvView c;
+  if (check_cache(cache, &c) != RFP2_OK || B < 1 || B > rfp2::kMaxAttnSeqs || B > c.seqs ||
+      new_tokens < 1 || new_tokens > RFP2_ATTN_MAX_NEW || H < 1 || H > 1024 || H % c.heads != 0)
+    return 0;
+  return rfp2::paged_attn_workspace_bytes(c.heads, c.dim, B, new_tokens, H);
+}
+
+rfp2_status rfp2_paged_attn(const rfp2_kv_cache* cache, const float* q, int64_t B,
+                            int64_t new_tokens, int64_t H, int64_t q_stride,
+                            const int32_t* lens, float scale, int64_t window, float* y,
+                            int32_t* err, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream) {
+  rfp2::KvView c;
+  const rfp2_status st = check_cache(cache, &c);
+  if (st != RFP2_OK) return st;
+  if (!q || !lens || !y || !workspace) return RFP2_E_NULL;
+  const size_t need = rfp2_paged_attn_workspace_bytes(cache, B, new_tokens, H);
+  if (need == 0 || workspace_bytes < need || !row_stride_ok(q_stride, H * c.dim) || window < 0 ||
+      !std::isfinite(scale))
+    return RFP2_E_SHAPE;
+  if (!aligned(q, 16) || !aligned(y, 16) || !aligned(lens, 4) || !aligned(workspace, 256) ||
+      (err && !aligned(err, 4)))
+    return RFP2_E_ALIGN;
+  (void)hipGetLastError();
+  return from_hip(rfp2::launch_paged_attn(c, cache->format == RFP2_KV_I8, q, B, new_tokens, H,
+                                          q_stride, lens, scale, window, y, err, workspace,
+                                          stream));
 }
 
 rfp2_status rfp2_read_ceiling(const uint8_t* buf, int64_t bytes, uint32_t magic, uint32_t* out,

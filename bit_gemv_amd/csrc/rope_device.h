@@ -1,0 +1,39 @@
+// Rotary positions inside a kernel: the workgroup computes the cosines and
+// sines of its token's angles once, into LDS, and every head is rotated with
+// them.
+//
+// Pair i of a head turns by the angle pos * f_i.  In fp32 the angle of
+// position 10^6 is off by 2^-24 * 10^6 = 0.06 radians, so it is formed in
+// fp64 and reduced to a fraction of a turn there; cosine, sine and the
+// rotation itself stay in fp64 too and the rotated value is rounded to fp32
+// once.  That makes the value reproducible (it is the correctly rounded one
+// but for ~2^-28 of the cases), which matters where it is quantized to int8
+// next: a last-bit difference would flip codes.  The fp64 work is one sincos
+// per pair and token and four multiplications and additions per pair and
+// head, under the time of the transfer.
+#pragma once
+
+#include "rfp2_internal.h"
+
+namespace rfp2 {
+
+// table[i] = mscale * (cos, sin) of pair i's angle at position pos; every
+// thread of the workgroup calls it, and a barrier follows before use.
+__device__ __forceinline__ void rope_table(double2* table, const RopeView& r, int32_t pos,
+                                           int tid, int threads) {
+  for (int i = tid; i < (r.rot >> 1); i += threads) {
+    double turns = (double)pos * r.freqs[i] * 0.15915494309189533577;   // 1 / (2 pi)
+    turns -= rint(turns);
+    double s, c;
+    sincospi(2.0 * turns, &s, &c);
+    table[i] = make_double2(r.mscale * c, r.mscale * s);
+  }
+}
+
+// (x1, x2) turned by one pair's cosine and sine.
+__device__ __forceinline__ float2 rope_turn(float x1, float x2, double2 cs) {
+  const double a = x1, b = x2;
+  return make_float2((float)(a * cs.x - b * cs.y), (float)(b * cs.x + a * cs.y));
+}
+
+}  // namespace rfp2

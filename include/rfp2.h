@@ -307,6 +307,173 @@ rfp2_status rfp2_quant_moe_gemv(const uint8_t* w, int64_t E, int64_t N, int64_t 
                                 hipStream_t stream);
 
 /*
+ * Rotary positions, a paged key/value cache and the attention over it: what a
+ * decode step does between its weight products.  The products' fp32 rows go
+ * in, the attention's fp32 rows come out and feed rfp2_quant_gemv or
+ * rfp2_quantize_acts.
+ *
+ * rfp2_rope_freqs -- the angle per position of each pair of a rotary
+ * embedding, written to freqs [rot/2] (device fp64, 8-byte aligned):
+ *   f_i = base^(-2i / rot), i = 0 .. rot/2 - 1, stretched for contexts longer
+ *   than the model was made for:
+ *   orig_len == 0   every f_i is divided by factor (linear interpolation);
+ *   orig_len > 0    by parts: with r_i = orig_len * f_i / (2 pi) turns over
+ *     the original length and g_i = clamp((r_i - low_turns) / (high_turns -
+ *     low_turns), 0, 1), the result is (1 - g_i) * f_i / factor + g_i * f_i
+ *     (slow pairs are interpolated, fast pairs are kept).
+ *   factor == 1 leaves f_i as it is in either form.
+ * Requires 2 <= rot <= 1024, rot even, base > 1, factor >= 1, orig_len >= 0,
+ * and 0 <= low_turns < high_turns where orig_len > 0; all finite.
+ */
+rfp2_status rfp2_rope_freqs(int64_t rot, double base, double factor, double orig_len,
+                            double low_turns, double high_turns, double* freqs,
+                            hipStream_t stream);
+
+/* Which two values of a head form pair i of `rot` rotated values. */
+#define RFP2_ROPE_HALF 0        /* i and i + rot/2  */
+#define RFP2_ROPE_INTERLEAVED 1 /* 2i and 2i + 1    */
+
+/*
+ * rfp2_rope -- rotary positions: the first rot values of every head are
+ * rotated pair by pair, the rest is copied.  With a = pos[t] * freqs[i]:
+ *   y1 = mscale * (x1 cos a - x2 sin a),  y2 = mscale * (x2 cos a + x1 sin a),
+ * computed in fp64 and rounded once, so that far positions keep their angle.
+ *   x   T rows of H heads of D fp32 values, row t at x + t * x_stride;
+ *       y likewise with y_stride.  y == x with equal strides rotates in
+ *       place; any other overlap is not allowed.  16-byte aligned.
+ *   pos [T] int32 on the device (4-byte aligned), any value.
+ *   freqs [rot/2] fp64 on the device, 8-byte aligned.
+ * Requires T >= 1, H >= 1, 4 <= D <= 1024, D % 4 == 0, 2 <= rot <= D, rot
+ * even, H * D <= 2^24, strides >= H * D and multiples of 4, a style of the
+ * two above, mscale finite.
+ */
+rfp2_status rfp2_rope(const float* x, int64_t T, int64_t H, int64_t D, int64_t x_stride,
+                      const int32_t* pos, const double* freqs, int64_t rot, int style,
+                      double mscale, float* y, int64_t y_stride, hipStream_t stream);
+
+/* What a cached value is held as. */
+#define RFP2_KV_F16 0 /* IEEE half precision                                    */
+#define RFP2_KV_I8 1  /* int8, one fp32 scale per 32 values of a token and head,
+                         code and scale exactly as rfp2_quantize_acts gives them */
+
+/*
+ * rfp2_kv_cache -- a paged key/value cache.  The struct itself lives in HOST
+ * memory and is read during the call; the pointers in it are device pointers
+ * owned by the caller.  Token p of sequence s is row p % page_size of page
+ * page_table[s * max_pages + p / page_size]; entries whose tokens no call
+ * touches may hold anything.  With H = kv_heads, D = head_dim, P = page_size:
+ *   k        [pages][H][P][D]        half or int8, 16-byte aligned
+ *   v        [pages][H][P/8][D][8]   the same type, 16-byte aligned: eight
+ *            tokens side by side for each value, the order in which the
+ *            attention's matrix instructions sum over tokens
+ *   k_scale, v_scale [pages][H][P/8][D/32][8] fp32, 16-byte aligned: the
+ *            scale of 32 values, eight tokens side by side (RFP2_KV_I8; not
+ *            read for RFP2_KV_F16)
+ *   page_table [seqs][max_pages] int32, 4-byte aligned
+ * Requires 1 <= kv_heads <= 1024, head_dim a multiple of 32 from 32 to 256,
+ * page_size a power of two from 8 to 4096, 1 <= pages < 2^31, 1 <= seqs <=
+ * 2^20, max_pages >= 1, max_pages * page_size < 2^31.  Offsets into the cache
+ * are computed in 64 bits.
+ */
+typedef struct rfp2_kv_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  int64_t seqs;
+  int64_t max_pages;
+  int64_t pages;
+  int64_t page_size;
+  int64_t kv_heads;
+  int64_t head_dim;
+  int32_t format;
+} rfp2_kv_cache;
+
+/*
+ * rfp2_kv_write -- T tokens' keys and values into the cache.
+ *   k, v  T rows of kv_heads heads of head_dim fp32 values, row t at
+ *         k + t * k_stride and v + t * v_stride; 16-byte aligned.
+ *   seq, pos [T] int32 on the device: token t is token pos[t] of sequence
+ *         seq[t].  pos[t] < 0 marks padding: nothing is stored.
+ *   err   nullable device int32: a token whose sequence, position or page lies
+ *         outside the cache is not stored and 1 is written to *err (never
+ *         cleared by the call).
+ * RFP2_KV_F16 rounds to nearest even (beyond 65504: infinity).  Where two
+ * tokens of a call name one place, either may remain.
+ * Requires T >= 1, strides >= kv_heads * head_dim and multiples of 4.
+ */
+rfp2_status rfp2_kv_write(const rfp2_kv_cache* cache, const float* k, const float* v, int64_t T,
+                          int64_t k_stride, int64_t v_stride, const int32_t* seq,
+                          const int32_t* pos, int32_t* err, hipStream_t stream);
+
+/*
+ * rfp2_rope_kv_write -- rfp2_rope of T tokens' H query heads and kv_heads key
+ * heads at positions pos, and rfp2_kv_write of the rotated keys and of the
+ * values, in one launch (the row of one QKV product: q, k and v may be parts
+ * of the same rows).  Bit-identical to the separate calls.  q_out (row t at
+ * q_out + t * q_out_stride) must not overlap q, k or v; it is written for
+ * every token, padding too.  H == 0 with q == q_out == NULL rotates and
+ * stores keys alone.
+ * Requires what the two calls require, and rot <= head_dim.
+ */
+rfp2_status rfp2_rope_kv_write(const rfp2_kv_cache* cache, const float* q, const float* k,
+                               const float* v, int64_t T, int64_t H, int64_t q_stride,
+                               int64_t k_stride, int64_t v_stride, const int32_t* seq,
+                               const int32_t* pos, const double* freqs, int64_t rot, int style,
+                               double mscale, float* q_out, int64_t q_out_stride, int32_t* err,
+                               hipStream_t stream);
+
+/*
+ * rfp2_kv_read -- T cached tokens back as fp32 (code * scale, or the half
+ * value): the reverse of rfp2_kv_write, with the same arguments.  pos[t] < 0
+ * gives a row of zeros; a token outside the cache gives a row of NaN and 1 is
+ * written to *err.
+ */
+rfp2_status rfp2_kv_read(const rfp2_kv_cache* cache, int64_t T, const int32_t* seq,
+                         const int32_t* pos, float* k, float* v, int64_t k_stride,
+                         int64_t v_stride, int32_t* err, hipStream_t stream);
+
+/*
+ * rfp2_paged_attn -- attention of each sequence's newest tokens over its
+ * cached tokens (its own keys and values already written).
+ *   Sequence b (row b of the page table) holds lens[b] tokens; its queries are
+ *   the tokens at positions lens[b] - new_tokens + t, t = 0 .. new_tokens - 1.
+ *   The query at position p sees the cached positions j with j <= p and, where
+ *   window > 0, j > p - window.  Query head h reads key/value head
+ *   h / (H / kv_heads):
+ *     y = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q.k_j - max).
+ *   q   [B][new_tokens] rows of H heads of head_dim fp32 values, row i at
+ *       q + i * q_stride; 16-byte aligned.
+ *   y   [B][new_tokens][H][head_dim] fp32, 16-byte aligned.  A query that sees
+ *       nothing (lens[b] <= 0, or a position below 0) gives zeros.
+ *   lens [B] int32 on the device; 4-byte aligned.
+ *   err nullable device int32: a length beyond max_pages * page_size, or a
+ *       visible token on a page outside the cache, gives NaN rows, and 1 is
+ *       written to *err (never cleared by the call).
+ *   workspace  device memory of at least rfp2_paged_attn_workspace_bytes(cache,
+ *       B, new_tokens, H) bytes, 256-byte aligned, owned by the caller;
+ *       overwritten.  Calls that share a workspace must not overlap in time.
+ * Scores, weights and sums are held in fp32; the queries and the weights enter
+ * the matrix cores as two half-precision numbers each (22 bits).  The result
+ * depends on nothing but the arguments (no atomics on values) and is the same
+ * from call to call.  What lies in the cache beyond a sequence's length never
+ * reaches an output.  Nothing is read back to the host, so the call can be
+ * captured in a graph and replayed with longer sequences.
+ * Requires 1 <= B <= min(1024, cache->seqs), 1 <= new_tokens <=
+ * RFP2_ATTN_MAX_NEW, H a multiple of kv_heads, H <= 1024, q_stride >= H *
+ * head_dim and a multiple of 4, window >= 0, scale finite.
+ */
+#define RFP2_ATTN_MAX_NEW 8
+size_t rfp2_paged_attn_workspace_bytes(const rfp2_kv_cache* cache, int64_t B,
+                                       int64_t new_tokens, int64_t H);
+rfp2_status rfp2_paged_attn(const rfp2_kv_cache* cache, const float* q, int64_t B,
+                            int64_t new_tokens, int64_t H, int64_t q_stride,
+                            const int32_t* lens, float scale, int64_t window, float* y,
+                            int32_t* err, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
+/*
  * rfp2_read_ceiling -- measurement helper, not part of the method: reads
  * `bytes` bytes of buf once with the plainest coalesced 16-byte loads
  * (thread t of the grid reads pieces t, t + T, t + 2T, ... of 16 bytes,
