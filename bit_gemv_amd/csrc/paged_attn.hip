@@ -1,114 +1,153 @@
-// Attention of each sequence's newest tokens over the paged key/value cache.
-//
-//   y = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q.k_j - m),
-//
-// over the visible cached tokens j, in one pass with a running maximum m: when
-// m grows, the sums so far are multiplied by exp(m_old - m_new).
-#include <hip/hip_fp16.h>
-
-#include "kv_device.h"
+// The paged attention's dispatch and the kernel that joins the shares' sums
+// (paged_attn.h holds the method, paged_attn_kernel.h the streaming kernel).
+#include "paged_attn.h"
 
 namespace rfp2 {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Row tiles of 16 query rows that one workgroup takes side by side.
+int row_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
-// One workgroup per query row (sequence, new token, head): 256 tokens at a
-// time, one per thread for the scores, one value per thread for the sums.
-template <bool I8>
-__global__ __launch_bounds__(kThreads) void paged_attn_kernel(
-    KvView c, const float* __restrict__ q, int T, int H, int64_t q_stride,
-    const int32_t* __restrict__ lens, float scale, int64_t window, float* __restrict__ y,
-    int32_t* __restrict__ err) {
-  __shared__ float qs[256];
-  __shared__ float w[kThreads];
-  __shared__ int64_t rows_of[kThreads];
-  __shared__ float red[kThreads / 64];
-  const int64_t row = blockIdx.x;                  // (b * T + t) * H + h
-  const int h = (int)(row % H);
-  const int64_t bt = row / H;
-  const int t = (int)(bt % T), b = (int)(bt / T);
-  const int D = c.dim, kvh = h / (H / c.heads), tid = threadIdx.x;
-  const int64_t len = lens[b];
-  const int64_t at = len - T + t;                  // this query's position
-  float* out = y + row * D;
-  if (len > ((int64_t)c.max_pages << c.page_shift)) {
-    if (err && tid == 0) *err = 1;
-    for (int d = tid; d < D; d += kThreads) out[d] = __builtin_nanf("");
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Layout {
+  size_t cum, ml, part, bytes;
+};
+
+Layout layout(int64_t dim, int64_t B, int64_t rows) {
+  const size_t slots = size_t(2) * kAttnGroups * std::min<int64_t>(rows, 16 * row_tiles(rows));
+  Layout l;
+  l.cum = 256;
+  l.ml = l.cum + round256(4 * (size_t)(B + 1));
+  l.part = l.ml + round256(slots * sizeof(float2));
+  l.bytes = l.part + round256(slots * (size_t)dim * sizeof(float));
+  return l;
+}
+
+// One workgroup per query row: the parts of its item, if there are several, are
+// summed with the weights exp2(m_i - m).  D / 4 lanes side by side take the
+// row's values, the rest of the workgroup other parts.  Also writes the rows
+// that no tile belongs to: sequences without tokens (zeros) or with an
+// impossible length (NaN).
+__global__ __launch_bounds__(kAttnThreads) void paged_attn_join_kernel(const AttnArgs a,
+                                                                       int rows_of_item) {
+  __shared__ float red[kAttnThreads / 64];
+  __shared__ float4 acc[kAttnThreads];
+  __shared__ float accl[kAttnThreads];
+  const int D = a.c.dim, tid = threadIdx.x;
+  const int64_t row = blockIdx.x;                   // (b * T + t) * H + h
+  const int h = (int)(row % a.H);
+  const int64_t bt = row / a.H;
+  const int t = (int)(bt % a.T), b = (int)(bt / a.T);
+  const int64_t nt = a.cum[b + 1] - a.cum[b];
+  const int lanes = D >> 2;                         // 8 .. 64
+  const int lane = tid % lanes, group = tid / lanes, groups = kAttnThreads / lanes;
+  const bool active = group < groups;
+  float4* out = reinterpret_cast<float4*>(a.y + row * D);
+  if (nt == 0) {
+    const float v = a.lens[b] > 0 ? __builtin_nanf("") : 0.0f;
+    if (tid < lanes) out[tid] = make_float4(v, v, v, v);
     return;
   }
-  for (int d = tid; d < D; d += kThreads) qs[d] = q[bt * q_stride + (int64_t)h * D + d];
-  float m = -INFINITY, l = 0.0f, acc = 0.0f;
-  const int64_t first = window > 0 && at >= window ? at - window + 1 : 0;
-  for (int64_t j0 = first; j0 <= at; j0 += kThreads) {
-    const int64_t j = j0 + tid;
-    float s = -INFINITY;
-    int64_t rows = 0;
-    __syncthreads();
-    if (j <= at) {
-      const int32_t page = kv_page(c, b, (int32_t)j);
-      const int r = (int)j & ((1 << c.page_shift) - 1);
-      if (page < 0) {
-        if (err) *err = 1;
-        s = __builtin_nanf("");
-      } else {
-        rows = kv_rows(c, page, kvh);
-        float dot = 0.0f;
-        for (int g = 0; g < D / 32; ++g) {
-          float part = 0.0f;
-          for (int d = 32 * g; d < 32 * g + 32; ++d) {
-            const int64_t e = k_at(c, rows, r, d);
-            part += qs[d] * (I8 ? (float)static_cast<const int8_t*>(c.k)[e]
-                                : __half2float(static_cast<const __half*>(c.k)[e]));
-          }
-          dot += I8 ? part * c.ks[scale_at(c, rows, r, g)] : part;
-        }
-        s = dot * scale;
-      }
-      rows += r;                                   // page rows and row in one number
-    }
-    rows_of[tid] = rows;
-    float mx = s;
-    for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
-    if ((tid & 63) == 0) red[tid >> 6] = mx;
-    __syncthreads();
-    const float m_new = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    w[tid] = j <= at ? expf(s - m_new) : 0.0f;
-    __syncthreads();
-    const float fix = m == m_new ? 1.0f : expf(m - m_new);
-    acc *= fix;
-    l *= fix;
-    m = m_new;
-    const int n = (int)min((int64_t)kThreads, at - j0 + 1);
-    for (int i = 0; i < n; ++i) {
-      const float p = w[i];
-      l += p;
-      if (tid < D) {
-        const int64_t rr = rows_of[i];
-        const int r = (int)(rr & 7);
-        const int64_t e = (rr - r) * D + tid * 8 + r;
-        acc += p * (I8 ? (float)static_cast<const int8_t*>(c.v)[e] *
-                             c.vs[(rr - r) * (D >> 5) + (tid >> 5) * 8 + r]
-                       : __half2float(static_cast<const __half*>(c.v)[e]));
-      }
+  const int kvh = h / a.group;
+  const int r = t * a.group + (h - kvh * a.group);
+  const int rg = r / rows_of_item;
+  const int64_t share = a.plan[0];
+  const int64_t items = (int64_t)a.c.heads * a.row_groups;
+  const int64_t first = (int64_t)a.cum[b] * items + (int64_t)(kvh * a.row_groups + rg) * nt;
+  const int64_t w0 = first / share, w1 = (first + nt - 1) / share;
+  if (w0 == w1) return;                             // written by its one workgroup
+  const int parts = (int)(w1 - w0 + 1);
+  // part i is slot 0 of workgroup w0 + i, but for a first one that starts inside its share
+  const int64_t r_in = r - rg * rows_of_item;
+  auto at = [&](int i) {
+    const int64_t w = w0 + i;
+    const int slot = i == 0 && first != w0 * share ? 1 : 0;
+    return (2 * w + slot) * a.slot_rows + r_in;
+  };
+  float m = -INFINITY;
+  for (int i = tid; i < parts; i += kAttnThreads) m = fmaxf(m, a.ml[at(i)].x);
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  if ((tid & 63) == 0) red[tid >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.0f;
+  if (active) {
+#pragma unroll 4
+    for (int i = group; i < parts; i += groups) {
+      const int64_t k = at(i);
+      const float2 ml = a.ml[k];
+      const float4 p = reinterpret_cast<const float4*>(a.part + k * D)[lane];
+      const float f = __builtin_amdgcn_exp2f(ml.x - m);
+      l += f * ml.y;
+      s.x += f * p.x; s.y += f * p.y; s.z += f * p.z; s.w += f * p.w;
     }
   }
-  if (tid < D) out[tid] = at < 0 ? 0.0f : acc / l;
+  acc[tid] = s;
+  accl[tid] = l;
+  __syncthreads();
+  if (tid < lanes) {
+    for (int i = 1; i < groups; ++i) {
+      const float4 p = acc[i * lanes + tid];
+      s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
+      l += accl[i * lanes + tid];
+    }
+    const float f = 1.0f / l;
+    const bool none = a.lens[b] - a.T + t < 0;      // a row that sees nothing
+    out[tid] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                    : make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
+  }
 }
 
 }  // namespace
 
-size_t paged_attn_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 256; }
+size_t paged_attn_workspace_bytes(int64_t kv_heads, int64_t dim, int64_t B, int64_t new_tokens,
+                                  int64_t H) {
+  return layout(dim, B, new_tokens * (H / kv_heads)).bytes;
+}
 
 hipError_t launch_paged_attn(const KvView& c, bool i8, const float* q, int64_t B,
                              int64_t new_tokens, int64_t H, int64_t q_stride,
                              const int32_t* lens, float scale, int64_t window, float* y,
                              int32_t* err, void* workspace, hipStream_t stream) {
-  (void)workspace;
-  const auto kernel = i8 ? paged_attn_kernel<true> : paged_attn_kernel<false>;
-  hipLaunchKernelGGL(kernel, dim3((uint32_t)(B * new_tokens * H)), dim3(kThreads), 0, stream, c,
-                     q, (int)new_tokens, (int)H, q_stride, lens, scale, window, y, err);
+  const int64_t group = H / c.heads, rows = new_tokens * group;
+  const int rw = row_tiles(rows);
+  const Layout l = layout(c.dim, B, rows);
+  char* ws = static_cast<char*>(workspace);
+  AttnArgs a;
+  a.c = c;
+  a.q = q;
+  a.lens = lens;
+  a.y = y;
+  a.err = err;
+  a.q_stride = q_stride;
+  a.window = window;
+  a.scale = scale;
+  a.B = (int)B;
+  a.T = (int)new_tokens;
+  a.H = (int)H;
+  a.group = (int)group;
+  a.row_groups = (int)((rows + 16 * rw - 1) / (16 * rw));
+  a.slot_rows = (int)std::min<int64_t>(rows, 16 * rw);
+  a.plan = reinterpret_cast<int64_t*>(ws);
+  a.cum = reinterpret_cast<uint32_t*>(ws + l.cum);
+  a.ml = reinterpret_cast<float2*>(ws + l.ml);
+  a.part = reinterpret_cast<float*>(ws + l.part);
+  // no more workgroups than shares of the longest lengths the page table allows
+  const int64_t tiles = ((((int64_t)c.max_pages << c.page_shift) + 31) / 32 + 1) * B * c.heads *
+                        a.row_groups;
+  const int grid = (int)std::min<int64_t>(kAttnGroups, (tiles + kAttnMinTiles - 1) / kAttnMinTiles);
+  const int nb = c.dim / 32;
+  const auto launch = nb <= 2   ? launch_paged_attn_12
+                      : nb <= 4 ? launch_paged_attn_34
+                      : nb <= 6 ? launch_paged_attn_56
+                                : launch_paged_attn_78;
+  hipError_t e = launch(a, i8, nb, rw, grid, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(paged_attn_join_kernel, dim3((uint32_t)(B * new_tokens * H)),
+                     dim3(kAttnThreads), 0, stream, a, 16 * rw);
   return hipGetLastError();
 }
 

@@ -1,0 +1,13 @@
+// The paged attention for heads of 224 and 256 values (a file of its own so that the
+// sizes compile side by side).
+#include "paged_attn_kernel.h"
+
+namespace rfp2 {
+
+hipError_t launch_paged_attn_78(const AttnArgs& a, bool i8, int nb, int rw, int grid,
+                                hipStream_t stream) {
+  return nb == 7 ? launch_attn_nb<7>(a, i8, rw, grid, stream)
+                 : launch_attn_nb<8>(a, i8, rw, grid, stream);
+}
+
+}  // namespace rfp2

@@ -337,7 +337,8 @@ size_t rfp2_paged_attn_workspace_bytes(const rfp2_kv_cache* cache, int64_t B, in
                                        int64_t H) {
   rfp2::KvView c;
   if (check_cache(cache, &c) != RFP2_OK || B < 1 || B > rfp2::kMaxAttnSeqs || B > c.seqs ||
-      new_tokens < 1 || new_tokens > RFP2_ATTN_MAX_NEW || H < 1 || H > 1024 || H % c.heads != 0)
+      new_tokens < 1 || new_tokens > RFP2_ATTN_MAX_NEW || H < 1 || H > 1024 || H % c.heads != 0 ||
+      B * cache->max_pages * cache->page_size > (int64_t(1) << 36))
     return 0;
   return rfp2::paged_attn_workspace_bytes(c.heads, c.dim, B, new_tokens, H);
 }

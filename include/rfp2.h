@@ -454,14 +454,14 @@ rfp2_status rfp2_kv_read(const rfp2_kv_cache* cache, int64_t T, const int32_t* s
  *   workspace  device memory of at least rfp2_paged_attn_workspace_bytes(cache,
  *       B, new_tokens, H) bytes, 256-byte aligned, owned by the caller;
  *       overwritten.  Calls that share a workspace must not overlap in time.
- * Scores, weights and sums are held in fp32; the queries and the weights enter
- * the matrix cores as two half-precision numbers each (22 bits).  The result
+ * Scores, weights and sums are held in fp32; the queries enter the matrix
+ * cores as two half-precision numbers each (22 bits of the row's largest).  The result
  * depends on nothing but the arguments (no atomics on values) and is the same
  * from call to call.  What lies in the cache beyond a sequence's length never
  * reaches an output.  Nothing is read back to the host, so the call can be
  * captured in a graph and replayed with longer sequences.
- * Requires 1 <= B <= min(1024, cache->seqs), 1 <= new_tokens <=
- * RFP2_ATTN_MAX_NEW, H a multiple of kv_heads, H <= 1024, q_stride >= H *
+ * Requires 1 <= B <= min(1024, cache->seqs), B * max_pages * page_size <=
+ * 2^36, 1 <= new_tokens <= RFP2_ATTN_MAX_NEW, H a multiple of kv_heads, H <= 1024, q_stride >= H *
  * head_dim and a multiple of 4, window >= 0, scale finite.
  */
 #define RFP2_ATTN_MAX_NEW 8

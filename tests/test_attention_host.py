@@ -129,6 +129,10 @@ def test_paged_attn():
                 dict(scale=math.nan), dict(ws_bytes=need - 1)):
         assert attn(cache(), **bad) == SHAPE, bad
     assert attn(cache(seqs=2000), B=1025) == SHAPE
+    # the tiles of all sequences together are counted in 32 bits
+    far = dict(seqs=1024, max_pages=(1 << 31) // 64 - 1)
+    assert attn(cache(**far), B=33) == SHAPE
+    assert rf.lib().rfp2_paged_attn_workspace_bytes(cache(**far), 32, 1, 32) > 0
     for bad in (dict(q=P + 4), dict(y=P + 4), dict(lens=P + 2), dict(err=P + 1), dict(ws=P + 64)):
         assert attn(cache(), **bad) == ALIGN, bad
     assert attn(None) == NULL
