@@ -24,6 +24,14 @@ __device__ __forceinline__ float row_bcast(float x) {
       __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + N, 0xF, 0xF, true));
 }
 
+// scale * x on its own: the broadcast folds into a multiplication, not into a
+// fused multiply-add, which would keep every broadcast scale in a register.
+__device__ __forceinline__ float scaled(float scale, float x) {
+#pragma clang fp contract(off)
+  const float y = scale * x;
+  return y;
+}
+
 __device__ __forceinline__ float max_over_groups(float x) {     // lanes l, l^16, l^32, l^48
   x = fmaxf(x, __shfl_xor(x, 16, 64));
   return fmaxf(x, __shfl_xor(x, 32, 64));
@@ -215,10 +223,15 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
 #pragma unroll
     for (int i = 0; i < 2 * NB; ++i) o[i] = float4v{0.f, 0.f, 0.f, 0.f};
     float m = kLowest, l = 0.0f;
-    Kreg kr[2][NB];
-    uint4 vr[I8 ? NB : 2 * NB];
-    float ksr[NW], vsr[NW];
-    bool bad = false;
+    struct Keys {                           // a tile's keys and their scales
+      Kreg r[2][NB];
+      float s[NW];
+    } key;
+    struct Values {                         // a tile's values, their scales, no such page
+      uint4 r[I8 ? NB : 2 * NB];
+      float s[NW];
+      bool bad;
+    } va, vb;
 
     // the page of token group `grp` (eight tokens), -1 where there is none
     auto page_of = [&](int grp) -> int32_t {
@@ -231,7 +244,7 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
       return kv_rows(a.c, page, kvh) + ((grp << 3) & ((1 << a.c.page_shift) - 1));
     };
     const int gk = n >> 2;                  // token group of this lane's key rows
-    auto load_k = [&](int tile, int32_t page) {
+    auto load_k = [&](int tile, int32_t page, int32_t page_s) {
       const bool ok = page >= 0 && page < a.c.pages;
       const int64_t r = rows_of(4 * tile + gk, ok ? page : 0) + (n & 3);
       const char* p = static_cast<const char*>(a.c.k) + (r * D + 8 * g) * ES;
@@ -239,39 +252,46 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int k = 0; k < NB; ++k)
-          kr[s][k] = *reinterpret_cast<const Kreg*>(p + (4 * s * D + 32 * k) * ES);
+          key.r[s][k] = *reinterpret_cast<const Kreg*>(p + (4 * s * D + 32 * k) * ES);
+      if constexpr (I8) {
+        const bool oks = page_s >= 0 && page_s < a.c.pages;
+        const int64_t rs = rows_of(4 * tile + g, oks ? page_s : 0);
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+          key.s[w] = a.c.ks[rs * NB + 16 * w + (2 * w + 1 < NB ? n : (n & 7))];
+      }
     };
-    auto load_v = [&](int tile, int32_t page) {
+    auto load_v = [&](Values& v, int tile, int32_t page) {
       const bool ok = page >= 0 && page < a.c.pages;
-      bad = !ok;
+      v.bad = !ok;
       const int64_t r = rows_of(4 * tile + g, ok ? page : 0);
       const char* p = static_cast<const char*>(a.c.v) + r * D * ES + 16 * n;
 #pragma unroll
       for (int k = 0; k < (I8 ? NB : 2 * NB); ++k)
-        vr[k] = *reinterpret_cast<const uint4*>(p + 256 * k);
+        v.r[k] = *reinterpret_cast<const uint4*>(p + 256 * k);
       if constexpr (I8) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const int64_t at = r * NB + 16 * w + (2 * w + 1 < NB ? n : (n & 7));
-          ksr[w] = a.c.ks[at];
-          vsr[w] = a.c.vs[at];
-        }
+        for (int w = 0; w < NW; ++w)
+          v.s[w] = a.c.vs[r * NB + 16 * w + (2 * w + 1 < NB ? n : (n & 7))];
       }
     };
 
     int t = t0 + wt;
-    int32_t pk = 0, pv = 0;
-    if (t < t1) {
-      pk = page_of(4 * (tile0 + t) + gk);
-      pv = page_of(4 * (tile0 + t) + g);
-      load_k(tile0 + t, pk);
-      load_v(tile0 + t, pv);
-      if (t + WT < t1) {
-        pk = page_of(4 * (tile0 + t + WT) + gk);
-        pv = page_of(4 * (tile0 + t + WT) + g);
+    int32_t pk = 0, pv = 0;                 // pages of the next tile's keys and values
+    auto next_pages = [&](int u) {
+      if (u < t1) {
+        pk = page_of(4 * (tile0 + u) + gk);
+        pv = page_of(4 * (tile0 + u) + g);
       }
+    };
+    if (t < t1) {
+      next_pages(t);
+      load_k(tile0 + t, pk, pv);
+      load_v(va, tile0 + t, pv);
+      next_pages(t + WT);
     }
-    for (; t < t1; t += WT) {
+    // One tile: its values lie in `v`, the next tile's go to `next`.
+    auto step = [&](Values& v, Values& next) {
       const int tile = tile0 + t;
       const bool more = t + WT < t1;
       // scores: s[4 s + i] of token 8 g + 4 s + i
@@ -282,47 +302,44 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
         if constexpr (I8) {
           unrolled<0, NB>([&](auto kc) {
             constexpr int k = kc;
-            const half8v kk = halves_of(kr[s][k]);
+            const half8v kk = halves_of(key.r[s][k]);
             float4v part = {0.f, 0.f, 0.f, 0.f};
             part = mfma(kk, qh[k], part);
             part = mfma(kk, ql[k], part);
             if (s == 0) {
               unrolled<0, 4>([&](auto ic) {
                 constexpr int i = ic;
-                acc[i] = __builtin_fmaf(row_bcast<(k & 1) * 8 + i>(ksr[k >> 1]), part[i], acc[i]);
+                acc[i] += scaled(row_bcast<(k & 1) * 8 + i>(key.s[k >> 1]), part[i]);
               });
             } else {
               unrolled<0, 4>([&](auto ic) {
                 constexpr int i = ic;
-                acc[i] = __builtin_fmaf(row_bcast<(k & 1) * 8 + 4 + i>(ksr[k >> 1]), part[i], acc[i]);
+                acc[i] += scaled(row_bcast<(k & 1) * 8 + 4 + i>(key.s[k >> 1]), part[i]);
               });
             }
           });
         } else {
 #pragma unroll
           for (int k = 0; k < NB; ++k) {
-            acc = mfma(halves_of(kr[s][k]), qh[k], acc);
-            acc = mfma(halves_of(kr[s][k]), ql[k], acc);
+            acc = mfma(halves_of(key.r[s][k]), qh[k], acc);
+            acc = mfma(halves_of(key.r[s][k]), ql[k], acc);
           }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[4 * s + i] = acc[i] * c;
       }
-      // the next tile's keys are on their way while this one's weights are used
-      int32_t pk2 = 0, pv2 = 0;
+      // the next tile's keys and values are on their way while this one is worked on
       if (more) {
-        load_k(tile + WT, pk);
-        if (t + 2 * WT < t1) {
-          pk2 = page_of(4 * (tile + 2 * WT) + gk);
-          pv2 = page_of(4 * (tile + 2 * WT) + g);
-        }
+        load_k(tile + WT, pk, pv);
+        load_v(next, tile + WT, pv);
+        next_pages(t + 2 * WT);
       }
 
       // visibility: only a tile at an end of the sequence or of a window has hidden tokens
       const int pos0 = 32 * tile + 8 * g;
       const bool edge = 32 * tile + 31 > len - a.T ||
                         (a.window > 0 && 32 * tile <= len - 1 - a.window);
-      if (bad) {
+      if (v.bad) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = __builtin_nanf("");
         if (a.err) *a.err = 1;
@@ -336,29 +353,30 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
           // scales of tokens that no row sees may hold anything
 #pragma unroll
           for (int w = 0; w < NW; ++w)
-            if (pos0 + (n & 7) >= len || pos0 + (n & 7) < lo) vsr[w] = 0.0f;
+            if (pos0 + (n & 7) >= len || pos0 + (n & 7) < lo) v.s[w] = 0.0f;
           // A weight of 0 does not cancel the NaN scale of a token that some rows do
           // not see: it is taken out, and its block is lost to the rows that do see it.
-          bool odd = false;
+          uint64_t odd[NW], any_odd = 0;
 #pragma unroll
-          for (int w = 0; w < NW; ++w) odd |= !(fabsf(vsr[w]) < INFINITY);
-          if (__any(odd)) {
-            unrolled<0, NB>([&](auto kc) {
-              constexpr int k = kc;
-              float lost = 0.0f;
-              unrolled<0, 8>([&](auto jc) {
-                constexpr int j = jc;
-                const float s = row_bcast<(k & 1) * 8 + j>(vsr[k >> 1]);
-                if (x[j] != -INFINITY && !(fabsf(s) < INFINITY)) lost = 1.0f;
-              });
-              if (max_over_groups(lost) > 0.0f) {
+          for (int w = 0; w < NW; ++w) any_odd |= odd[w] = __ballot(!(fabsf(v.s[w]) < INFINITY));
+          if (any_odd) {
+            uint32_t seen = 0, lost = 0;                     // tokens; blocks
+#pragma unroll
+            for (int j = 0; j < 8; ++j) seen |= (x[j] != -INFINITY ? 1u : 0u) << j;
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+              if ((uint32_t)(odd[k >> 1] >> (16 * g + 8 * (k & 1))) & seen) lost |= 1u << k;
+            lost |= __shfl_xor(lost, 16, 64);
+            lost |= __shfl_xor(lost, 32, 64);
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+              if (lost >> k & 1) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[2 * k + i / 4][i % 4] = __builtin_nanf("");
               }
-            });
 #pragma unroll
             for (int w = 0; w < NW; ++w)
-              if (!(fabsf(vsr[w]) < INFINITY)) vsr[w] = 0.0f;
+              if (!(fabsf(v.s[w]) < INFINITY)) v.s[w] = 0.0f;
           }
         }
       }
@@ -387,12 +405,12 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
       if constexpr (I8) {
         unrolled<0, NB>([&](auto kc) {
           constexpr int k = kc;
-          const uint4 v = vr[k];
+          const uint4 c4 = v.r[k];
           unrolled<0, 8>([&](auto jc) {
             constexpr int j = jc;
-            const float w = row_bcast<(k & 1) * 8 + j>(vsr[k >> 1]) * p[j];
-            o[2 * k] = mfma4(code_of<j & 3>(j < 4 ? v.x : v.y), w, o[2 * k]);
-            o[2 * k + 1] = mfma4(code_of<j & 3>(j < 4 ? v.z : v.w), w, o[2 * k + 1]);
+            const float w = row_bcast<(k & 1) * 8 + j>(v.s[k >> 1]) * p[j];
+            o[2 * k] = mfma4(code_of<j & 3>(j < 4 ? c4.x : c4.y), w, o[2 * k]);
+            o[2 * k + 1] = mfma4(code_of<j & 3>(j < 4 ? c4.z : c4.w), w, o[2 * k + 1]);
           });
         });
       } else {
@@ -404,7 +422,7 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
           bool odd = false;
 #pragma unroll
           for (int k = 0; k < 2 * NB; ++k) {
-            const uint32_t w[4] = {vr[k].x, vr[k].y, vr[k].z, vr[k].w};
+            const uint32_t w[4] = {v.r[k].x, v.r[k].y, v.r[k].z, v.r[k].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               odd |= (w[i] & 0x7C00u) == 0x7C00u || (w[i] & 0x7C000000u) == 0x7C000000u;
@@ -415,13 +433,13 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
             for (int j = 0; j < 8; ++j) seen[j] = (_Float16)(x[j] == -INFINITY ? 0.0f : 1.0f);
 #pragma unroll
             for (int k = 0; k < 2 * NB; ++k) {
-              half8v v = halves_of(vr[k]), up, dn;
+              half8v f8 = halves_of(v.r[k]), up, dn;
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const float f = (float)v[j];
+                const float f = (float)f8[j];
                 up[j] = (_Float16)(f < INFINITY ? 0.0f : 1.0f);
                 dn[j] = (_Float16)(f > -INFINITY ? 0.0f : 1.0f);
-                if (!(fabsf(f) < INFINITY)) v[j] = (_Float16)0.0f;
+                if (!(fabsf(f) < INFINITY)) f8[j] = (_Float16)0.0f;
               }
               const float4v zero = {0.f, 0.f, 0.f, 0.f};
               const float4v nu = mfma(up, seen, zero), nd = mfma(dn, seen, zero);
@@ -431,23 +449,23 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
                 if (nd[i] > 0.0f) o[k][i] -= INFINITY;
               }
               union { half8v v; uint4 u; } back;
-              back.v = v;
-              vr[k] = back.u;
+              back.v = f8;
+              v.r[k] = back.u;
             }
           }
         }
 #pragma unroll
         for (int k = 0; k < 2 * NB; ++k) {
-          const half8v v = halves_of(vr[k]);
+          const half8v f8 = halves_of(v.r[k]);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[k] = mfma4((float)v[j], p[j], o[k]);
+          for (int j = 0; j < 8; ++j) o[k] = mfma4((float)f8[j], p[j], o[k]);
         }
       }
-      if (more) {
-        load_v(tile + WT, pv);
-        pk = pk2;
-        pv = pv2;
-      }
+      t += WT;
+    };
+    while (t < t1) {
+      step(va, vb);
+      if (t < t1) step(vb, va);
     }
 
     // ---- the waves' sums together, then out: finished, or into this share's slot
