@@ -121,7 +121,7 @@ def header_symbols() -> list[str]:
 def _stream(stream):
     import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -132,7 +132,7 @@ def _ptr(t, dtype, numel: int, name: str):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU (got {t.device})")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
@@ -398,13 +398,18 @@ def _rows(t, T: int, width: int, name: str):
         raise ValueError(f"{name} must live on the GPU (got {t.device})")
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be torch.float32 (got {t.dtype})")
-    if t.dim() < 2 or t.shape[0] < T:
-        raise ValueError(f"{name} must have {T} or more rows (shape {tuple(t.shape)})")
-    row = t[0]
-    if not row.is_contiguous() or row.numel() < width:
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 2 or shape[0] < T:
+        raise ValueError(f"{name} must have {T} or more rows (shape {tuple(shape)})")
+    row = 1
+    for n, s in zip(shape[:0:-1], strides[:0:-1]):
+        if n != 1 and s != row:
+            row = -1
+            break
+        row *= n
+    if row < width:
         raise ValueError(f"a row of {name} must be {width} or more contiguous values")
-    stride = t.stride(0)
-    return t.data_ptr(), stride if T > 1 else max(stride, width)
+    return t.data_ptr(), strides[0] if T > 1 else width
 
 
 def rfp2_rope_freqs(rot: int, base: float, factor: float, orig_len: float, low_turns: float,

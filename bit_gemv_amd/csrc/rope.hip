@@ -23,33 +23,84 @@ __global__ __launch_bounds__(kThreads) void rope_freqs_kernel(int n, double rot,
 }
 
 // One workgroup turns heads [blockIdx.y * per, ...) of token blockIdx.x.  A
-// thread owns whole pairs, read before they are written, so x may be y.
+// thread owns a unit of a head and takes every head's: four pairs of the half
+// style (V4: two 16-byte accesses), two neighbouring pairs of the interleaved one
+// (V4: one access), or one pair; past the rotated part, four values (V4) or one
+// that are copied.  Its pairs are read before they are written, so x may be y.
+template <bool INTER, bool V4>
 __global__ __launch_bounds__(kThreads) void rope_kernel(const float* x, int H, int D,
                                                         int64_t x_stride,
                                                         const int32_t* __restrict__ pos,
                                                         RopeView r, float* y, int64_t y_stride,
                                                         int per) {
   __shared__ double2 table[kMaxRopeDim / 2];
+  constexpr int PAIRS = V4 ? (INTER ? 2 : 4) : 1;     // of a unit
+  constexpr int COPY = V4 ? 4 : 1;                    // values of a unit that is copied
+  constexpr int BATCH = 4;                            // heads whose values are in flight
   const int64_t t = blockIdx.x;
-  rope_table(table, r, pos[t], threadIdx.x, kThreads);
-  __syncthreads();
-  const int h0 = blockIdx.y * per, h1 = min(H, h0 + per);
+  const int half = r.rot >> 1, tid = threadIdx.x;
+  const int h1 = min(H, ((int)blockIdx.y + 1) * per);
+  const int turning = half / PAIRS, units = turning + (D - r.rot) / COPY;
   const float* xr = x + t * x_stride;
   float* yr = y + t * y_stride;
-  const int half = r.rot >> 1;
-  const int units = half + (D - r.rot);     // pairs, then single values that are copied
-  for (int u = threadIdx.x; u < (h1 - h0) * units; u += kThreads) {
-    const int h = u / units, i = u - h * units;
-    const int64_t base = (int64_t)(h0 + h) * D;
-    if (i < half) {
-      const int64_t a = base + (r.interleaved ? 2 * i : i);
-      const int64_t b = r.interleaved ? a + 1 : a + half;
-      const float2 o = rope_turn(xr[a], xr[b], table[i]);
-      yr[a] = o.x;
-      yr[b] = o.y;
-    } else {
-      const int64_t a = base + r.rot + (i - half);
-      yr[a] = xr[a];
+  const int width = min(units, kThreads), slots = kThreads / width, slot = tid / width;
+  const int lane = tid - slot * width;
+  const int32_t p = pos[t];
+  for (int i = tid; i < half; i += kThreads) table[i] = rope_entry(r, p, i);
+  __syncthreads();
+  if (slot >= slots) return;
+  for (int u = lane; u < units; u += width) {
+    const bool turns = u < turning;
+    const int a = turns ? (INTER ? 2 : 1) * PAIRS * u : r.rot + COPY * (u - turning);
+    double2 cs[PAIRS];
+    if (turns) {
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) cs[i] = table[PAIRS * u + i];
+    }
+    for (int hb = blockIdx.y * per + slot; hb < h1; hb += BATCH * slots) {
+      float4 lo[BATCH], hi[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int h = hb + k * slots;
+        if (h >= h1) continue;
+        const float* s = xr + (int64_t)h * D + a;
+        if constexpr (V4) {
+          lo[k] = *reinterpret_cast<const float4*>(s);
+          if (!INTER && turns) hi[k] = *reinterpret_cast<const float4*>(s + half);
+        } else {
+          lo[k].x = s[0];
+          if (turns) hi[k].x = s[INTER ? 1 : half];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int h = hb + k * slots;
+        if (h >= h1) continue;
+        float* o = yr + (int64_t)h * D + a;
+        float4 l = lo[k], g = hi[k];
+        if (turns) {
+          if constexpr (V4 && INTER) {
+            const float2 u0 = rope_turn(l.x, l.y, cs[0]), u1 = rope_turn(l.z, l.w, cs[1]);
+            l = make_float4(u0.x, u0.y, u1.x, u1.y);
+          } else if constexpr (V4) {
+            const float2 u0 = rope_turn(l.x, g.x, cs[0]), u1 = rope_turn(l.y, g.y, cs[1]),
+                         u2 = rope_turn(l.z, g.z, cs[2]), u3 = rope_turn(l.w, g.w, cs[3]);
+            l = make_float4(u0.x, u1.x, u2.x, u3.x);
+            g = make_float4(u0.y, u1.y, u2.y, u3.y);
+          } else {
+            const float2 u0 = rope_turn(l.x, g.x, cs[0]);
+            l.x = u0.x;
+            g.x = u0.y;
+          }
+        }
+        if constexpr (V4) {
+          *reinterpret_cast<float4*>(o) = l;
+          if (!INTER && turns) *reinterpret_cast<float4*>(o + half) = g;
+        } else {
+          o[0] = l.x;
+          if (turns) o[INTER ? 1 : half] = g.x;
+        }
+      }
     }
   }
 }
@@ -69,10 +120,17 @@ hipError_t launch_rope_freqs(int64_t rot, double base, double factor, double ori
 hipError_t launch_rope(const float* x, int64_t T, int64_t H, int64_t D, int64_t x_stride,
                        const int32_t* pos, const RopeView& rope, float* y, int64_t y_stride,
                        hipStream_t stream) {
-  const int per = (int)H;
-  hipLaunchKernelGGL(rope_kernel, dim3((uint32_t)T, (uint32_t)((H + per - 1) / per)),
-                     dim3(kThreads), 0, stream, x, (int)H, (int)D, x_stride, pos, rope, y,
-                     y_stride, per);
+  // 16-byte accesses where the pairs allow them
+  const bool inter = rope.interleaved != 0;
+  const bool v4 = rope.rot % (inter ? 4 : 8) == 0;
+  const int units = rope.rot / (v4 ? (inter ? 4 : 8) : 2) + ((int)D - rope.rot) / (v4 ? 4 : 1);
+  // A workgroup takes all heads of its token (the angles are computed once) unless
+  // few tokens would leave compute units idle: then one head a thread.
+  const int per = T >= 512 ? (int)H : std::max(1, kThreads / std::min(units, kThreads));
+  const auto kernel = inter ? (v4 ? rope_kernel<true, true> : rope_kernel<true, false>)
+                            : (v4 ? rope_kernel<false, true> : rope_kernel<false, false>);
+  hipLaunchKernelGGL(kernel, dim3((uint32_t)T, (uint32_t)((H + per - 1) / per)), dim3(kThreads),
+                     0, stream, x, (int)H, (int)D, x_stride, pos, rope, y, y_stride, per);
   return hipGetLastError();
 }
 

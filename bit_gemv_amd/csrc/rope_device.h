@@ -17,17 +17,13 @@
 
 namespace rfp2 {
 
-// table[i] = mscale * (cos, sin) of pair i's angle at position pos; every
-// thread of the workgroup calls it, and a barrier follows before use.
-__device__ __forceinline__ void rope_table(double2* table, const RopeView& r, int32_t pos,
-                                           int tid, int threads) {
-  for (int i = tid; i < (r.rot >> 1); i += threads) {
-    double turns = (double)pos * r.freqs[i] * 0.15915494309189533577;   // 1 / (2 pi)
-    turns -= rint(turns);
-    double s, c;
-    sincospi(2.0 * turns, &s, &c);
-    table[i] = make_double2(r.mscale * c, r.mscale * s);
-  }
+// mscale * (cos, sin) of pair i's angle at position pos.
+__device__ __forceinline__ double2 rope_entry(const RopeView& r, int32_t pos, int i) {
+  double turns = (double)pos * r.freqs[i] * 0.15915494309189533577;   // 1 / (2 pi)
+  turns -= rint(turns);
+  double s, c;
+  sincospi(2.0 * turns, &s, &c);
+  return make_double2(r.mscale * c, r.mscale * s);
 }
 
 // (x1, x2) turned by one pair's cosine and sine.
