@@ -74,13 +74,13 @@ struct AttnArgs {
   float* part;                            // [groups][2][slot_rows][D] sums
 };
 
-hipError_t launch_paged_attn_12(const AttnArgs& a, bool i8, int nb, int rw, int grid,
+hipError_t launch_paged_attn_12(const AttnArgs& a, bool i8, int nb, int rows, int grid,
                                 hipStream_t stream);
-hipError_t launch_paged_attn_34(const AttnArgs& a, bool i8, int nb, int rw, int grid,
+hipError_t launch_paged_attn_34(const AttnArgs& a, bool i8, int nb, int rows, int grid,
                                 hipStream_t stream);
-hipError_t launch_paged_attn_56(const AttnArgs& a, bool i8, int nb, int rw, int grid,
+hipError_t launch_paged_attn_56(const AttnArgs& a, bool i8, int nb, int rows, int grid,
                                 hipStream_t stream);
-hipError_t launch_paged_attn_78(const AttnArgs& a, bool i8, int nb, int rw, int grid,
+hipError_t launch_paged_attn_78(const AttnArgs& a, bool i8, int nb, int rows, int grid,
                                 hipStream_t stream);
 
 }  // namespace rfp2

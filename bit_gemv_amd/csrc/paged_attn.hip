@@ -6,8 +6,10 @@ namespace rfp2 {
 
 namespace {
 
-// Row tiles of 16 query rows that one workgroup takes side by side.
-int row_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Query rows of an item: what the kernel variant that launch_attn picks takes at once.
+int item_rows(int64_t rows) {
+  return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -16,7 +18,7 @@ struct Layout {
 };
 
 Layout layout(int64_t dim, int64_t B, int64_t rows) {
-  const size_t slots = size_t(2) * kAttnGroups * std::min<int64_t>(rows, 16 * row_tiles(rows));
+  const size_t slots = size_t(2) * kAttnGroups * std::min<int64_t>(rows, item_rows(rows));
   Layout l;
   l.cum = 256;
   l.ml = l.cum + round256(4 * (size_t)(B + 1));
@@ -113,7 +115,7 @@ hipError_t launch_paged_attn(const KvView& c, bool i8, const float* q, int64_t B
                              const int32_t* lens, float scale, int64_t window, float* y,
                              int32_t* err, void* workspace, hipStream_t stream) {
   const int64_t group = H / c.heads, rows = new_tokens * group;
-  const int rw = row_tiles(rows);
+  const int ir = item_rows(rows);
   const Layout l = layout(c.dim, B, rows);
   char* ws = static_cast<char*>(workspace);
   AttnArgs a;
@@ -129,8 +131,8 @@ hipError_t launch_paged_attn(const KvView& c, bool i8, const float* q, int64_t B
   a.T = (int)new_tokens;
   a.H = (int)H;
   a.group = (int)group;
-  a.row_groups = (int)((rows + 16 * rw - 1) / (16 * rw));
-  a.slot_rows = (int)std::min<int64_t>(rows, 16 * rw);
+  a.row_groups = (int)((rows + ir - 1) / ir);
+  a.slot_rows = (int)std::min<int64_t>(rows, ir);
   a.plan = reinterpret_cast<int64_t*>(ws);
   a.cum = reinterpret_cast<uint32_t*>(ws + l.cum);
   a.ml = reinterpret_cast<float2*>(ws + l.ml);
@@ -144,10 +146,10 @@ hipError_t launch_paged_attn(const KvView& c, bool i8, const float* q, int64_t B
                       : nb <= 4 ? launch_paged_attn_34
                       : nb <= 6 ? launch_paged_attn_56
                                 : launch_paged_attn_78;
-  hipError_t e = launch(a, i8, nb, rw, grid, stream);
+  hipError_t e = launch(a, i8, nb, (int)std::min<int64_t>(rows, 64), grid, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(paged_attn_join_kernel, dim3((uint32_t)(B * new_tokens * H)),
-                     dim3(kAttnThreads), 0, stream, a, 16 * rw);
+                     dim3(kAttnThreads), 0, stream, a, ir);
   return hipGetLastError();
 }
 

@@ -4,10 +4,10 @@
 
 namespace rfp2 {
 
-hipError_t launch_paged_attn_12(const AttnArgs& a, bool i8, int nb, int rw, int grid,
+hipError_t launch_paged_attn_12(const AttnArgs& a, bool i8, int nb, int rows, int grid,
                                 hipStream_t stream) {
-  return nb == 1 ? launch_attn_nb<1>(a, i8, rw, grid, stream)
-                 : launch_attn_nb<2>(a, i8, rw, grid, stream);
+  return nb == 1 ? launch_attn_nb<1>(a, i8, rows, grid, stream)
+                 : launch_attn_nb<2>(a, i8, rows, grid, stream);
 }
 
 }  // namespace rfp2

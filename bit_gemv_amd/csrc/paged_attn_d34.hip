@@ -4,10 +4,10 @@
 
 namespace rfp2 {
 
-hipError_t launch_paged_attn_34(const AttnArgs& a, bool i8, int nb, int rw, int grid,
+hipError_t launch_paged_attn_34(const AttnArgs& a, bool i8, int nb, int rows, int grid,
                                 hipStream_t stream) {
-  return nb == 3 ? launch_attn_nb<3>(a, i8, rw, grid, stream)
-                 : launch_attn_nb<4>(a, i8, rw, grid, stream);
+  return nb == 3 ? launch_attn_nb<3>(a, i8, rows, grid, stream)
+                 : launch_attn_nb<4>(a, i8, rows, grid, stream);
 }
 
 }  // namespace rfp2

@@ -80,29 +80,61 @@ __device__ __forceinline__ float4v mfma(half8v a, half8v b, float4v c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// Sixteen products of 4 x 1 by 1 x 4 (lane 4 b + i holds row i, or column i, of
+// block b); the left operand of all eight blocks of a half of the wave is the one of
+// the half's block B.
+template <int B>
 __device__ __forceinline__ float4v mfma4(float a, float b, float4v c) {
-  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_4x4x1f32(a, b, c, 3, B, 0);
 }
 
-// Byte B of a word as a signed number.
-template <int B>
-__device__ __forceinline__ float code_of(uint32_t w) {
-  return (float)((int32_t)(w << (24 - 8 * B)) >> 24);
+// Value J of eight codes or halves.
+template <int J>
+__device__ __forceinline__ float value_of(uint2 w) {
+  const uint32_t u = J < 4 ? w.x : w.y;
+  return (float)((int32_t)(u << (24 - 8 * (J & 3))) >> 24);
+}
+template <int J>
+__device__ __forceinline__ float value_of(uint4 w) {
+  return (float)halves_of(w)[J];
+}
+
+__device__ __forceinline__ float lane_of(float x, int lane) {
+  return __int_as_float(__builtin_amdgcn_ds_bpermute(4 * lane, __float_as_int(x)));
+}
+
+// a / b where both mostly fit 32 bits
+__device__ __forceinline__ int64_t divided(int64_t a, int64_t b) {
+  return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// LDS written by some lanes of a wave, read by others of it: the accesses execute in
+// order, the compiler has to keep them so.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 constexpr float kLowest = -3.0e38f;        // the running maximum before any score
 constexpr float kSlack = 8.0f;             // weights may grow to 2^8 before sums are rescaled
 
-template <bool I8, int NB, int RW>
+// Q: groups of four query rows of a wave (1, 2 or 4); RW as described in paged_attn.h.
+template <bool I8, int NB, int Q, int RW>
 __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_kernel(
     const AttnArgs a) {
-  constexpr int D = 32 * NB, WT = 4 / RW, ROWS = 16 * RW, NW = (NB + 1) / 2;
+  constexpr int D = 32 * NB, WT = 4 / RW, WROWS = 4 * Q, ROWS = WROWS * RW, NW = (NB + 1) / 2;
+  constexpr int C = NB / 2;                 // whole chunks of 64 values
+  constexpr bool HALF = NB % 2 != 0;        // and a chunk of 32
+  constexpr int CA = C + (HALF ? 1 : 0);
   constexpr int ES = I8 ? 1 : 2;
-  using Kreg = std::conditional_t<I8, uint2, uint4>;
+  using Reg = std::conditional_t<I8, uint2, uint4>;   // eight codes or halves
   __shared__ uint32_t cum[kMaxAttnSeqs + 1];
+  __shared__ int32_t len_of[kMaxAttnSeqs];
   __shared__ uint32_t wave_sum[4];
-  __shared__ float2 wave_ml[4][16];
-  __shared__ float sums[4][16][D + 4];
+  __shared__ float2 wave_ml[4][WROWS];
+  __shared__ float sums[4][WROWS][D + 4];
+  __shared__ float weights[4][WROWS][36];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -118,26 +150,31 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
       const int b = 4 * tid + i;
       nt[i] = 0;
       if (b < a.B) {
-        const int64_t len = a.lens[b];
+        const int32_t len = a.lens[b];
+        len_of[b] = len;
         if (len > cap) {
           if (a.err && blockIdx.x == 0) *a.err = 1;
         } else if (len > 0) {
           const int64_t lo = a.window > 0 ? max((int64_t)0, len - a.T - a.window + 1) : 0;
-          nt[i] = (uint32_t)(((len + 31) >> 5) - (lo >> 5));
+          nt[i] = (uint32_t)((((int64_t)len + 31) >> 5) - (lo >> 5));
         }
       }
       mine += nt[i];
     }
     uint32_t inc = mine;
+    if (a.B > 4) {
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const uint32_t o = __shfl_up(inc, off, 64);
-      if (lane >= off) inc += o;
+      for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t o = __shfl_up(inc, off, 64);
+        if (lane >= off) inc += o;
+      }
     }
-    if (lane == 63) wave_sum[wave] = inc;
-    __syncthreads();
     uint32_t at = inc - mine;
-    for (int w = 0; w < wave; ++w) at += wave_sum[w];
+    if (a.B > 256) {
+      if (lane == 63) wave_sum[wave] = inc;
+      __syncthreads();
+      for (int w = 0; w < wave; ++w) at += wave_sum[w];
+    }
     if (tid == 0) cum[0] = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -149,7 +186,7 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
   const int items = a.c.heads * a.row_groups;
   const int64_t total = (int64_t)cum[a.B] * items;
   const int64_t share =
-      max((int64_t)kAttnMinTiles, (total + (int64_t)gridDim.x - 1) / (int64_t)gridDim.x);
+      max((int64_t)kAttnMinTiles, divided(total + (int64_t)gridDim.x - 1, (int64_t)gridDim.x));
   if (blockIdx.x == 0) {
     if (tid == 0) a.plan[0] = share;
     for (int b = tid; b <= a.B; b += kAttnThreads) a.cum[b] = cum[b];
@@ -170,7 +207,7 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
     while (unit >= (int64_t)cum[b + 1] * items) ++b;        // sequences without tiles
     const int64_t nt = cum[b + 1] - cum[b];
     const int64_t in_seq = unit - (int64_t)cum[b] * items;
-    const int item = (int)(in_seq / nt);
+    const int item = (int)divided(in_seq, nt);
     const int t0 = (int)(in_seq - item * nt);
     const int t1 = (int)min(nt, t0 + (end_unit - unit));
     const bool whole = t0 == 0 && t1 == nt;
@@ -179,56 +216,18 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
 
     const int kvh = item / a.row_groups, rg = item - kvh * a.row_groups;
     const int rows_all = a.T * a.group;
-    const int len = a.lens[b];
+    const int len = __builtin_amdgcn_readfirstlane(len_of[b]);
     const int lo = a.window > 0 ? (int)max((int64_t)0, len - a.T - a.window + 1) : 0;
     const int tile0 = lo >> 5;
     const int group_lo = lo >> 3, group_hi = (len - 1) >> 3;
 
-    // ---- the query rows: row n of this wave's tile, as two halves, scaled by 2^(14 - ex)
-    const int row = rg * ROWS + wr * 16 + n;
-    const bool row_ok = row < rows_all;
-    const int row_t = row_ok ? row / a.group : 0;
-    const int row_h = kvh * a.group + (row_ok ? row - row_t * a.group : 0);
-    const int row_pos = len - a.T + row_t;                  // this row's position
-    half8v qh[NB], ql[NB];
-    float c;                                                // score -> base 2, unscaled
-    {
-      const float* qp = a.q + ((int64_t)b * a.T + row_t) * a.q_stride + (int64_t)row_h * D + 8 * g;
-      float x[NB][8], big = 0.0f;
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const float4 u = row_ok ? *reinterpret_cast<const float4*>(qp + 32 * k)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 v = row_ok ? *reinterpret_cast<const float4*>(qp + 32 * k + 4)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[k][0] = u.x; x[k][1] = u.y; x[k][2] = u.z; x[k][3] = u.w;
-        x[k][4] = v.x; x[k][5] = v.y; x[k][6] = v.z; x[k][7] = v.w;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[k][i]));
-      }
-      big = max_over_groups(big);
-      int ex = 0;
-      if (big > 0.0f && big < INFINITY) ex = max(ilogbf(big) + 1, -100);
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[k][i] = ldexpf(x[k][i], 14 - ex);
-        split8(x[k], qh[k], ql[k]);
-      }
-      c = ldexpf(a.scale * 1.44269504088896340736f, ex - 14);
-    }
-
-    // ---- the stream of tiles
-    float4v o[2 * NB];
-#pragma unroll
-    for (int i = 0; i < 2 * NB; ++i) o[i] = float4v{0.f, 0.f, 0.f, 0.f};
-    float m = kLowest, l = 0.0f;
+    // ---- the cache's tiles
     struct Keys {                           // a tile's keys and their scales
-      Kreg r[2][NB];
+      Reg r[2][NB];
       float s[NW];
     } key;
     struct Values {                         // a tile's values, their scales, no such page
-      uint4 r[I8 ? NB : 2 * NB];
+      Reg r[4][C > 0 ? C : 1], h[2];
       float s[NW];
       bool bad;
     } va, vb;
@@ -238,41 +237,54 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
       grp = min(max(grp, group_lo), group_hi);
       return a.c.table[(int64_t)b * a.c.max_pages + ((grp << 3) >> a.c.page_shift)];
     };
+    auto is_page = [&](int32_t page) { return page >= 0 && page < a.c.pages; };
     // rows before token group `grp` in the cache, given its page
     auto rows_of = [&](int grp, int32_t page) -> int64_t {
       grp = min(max(grp, group_lo), group_hi);
-      return kv_rows(a.c, page, kvh) + ((grp << 3) & ((1 << a.c.page_shift) - 1));
+      return kv_rows(a.c, is_page(page) ? page : 0, kvh) +
+             ((grp << 3) & ((1 << a.c.page_shift) - 1));
     };
     const int gk = n >> 2;                  // token group of this lane's key rows
     auto load_k = [&](int tile, int32_t page, int32_t page_s) {
-      const bool ok = page >= 0 && page < a.c.pages;
-      const int64_t r = rows_of(4 * tile + gk, ok ? page : 0) + (n & 3);
+      const int64_t r = rows_of(4 * tile + gk, page) + (n & 3);
       const char* p = static_cast<const char*>(a.c.k) + (r * D + 8 * g) * ES;
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int k = 0; k < NB; ++k)
-          key.r[s][k] = *reinterpret_cast<const Kreg*>(p + (4 * s * D + 32 * k) * ES);
+          key.r[s][k] = *reinterpret_cast<const Reg*>(p + (4 * s * D + 32 * k) * ES);
       if constexpr (I8) {
-        const bool oks = page_s >= 0 && page_s < a.c.pages;
-        const int64_t rs = rows_of(4 * tile + g, oks ? page_s : 0);
+        const int64_t rs = rows_of(4 * tile + g, page_s);
 #pragma unroll
         for (int w = 0; w < NW; ++w)
           key.s[w] = a.c.ks[rs * NB + 16 * w + (2 * w + 1 < NB ? n : (n & 7))];
       }
     };
     auto load_v = [&](Values& v, int tile, int32_t page) {
-      const bool ok = page >= 0 && page < a.c.pages;
-      v.bad = !ok;
-      const int64_t r = rows_of(4 * tile + g, ok ? page : 0);
-      const char* p = static_cast<const char*>(a.c.v) + r * D * ES + 16 * n;
+      v.bad = !is_page(page);
+      int64_t r[4];                         // the four token groups, the same for all lanes
 #pragma unroll
-      for (int k = 0; k < (I8 ? NB : 2 * NB); ++k)
-        v.r[k] = *reinterpret_cast<const uint4*>(p + 256 * k);
+      for (int u = 0; u < 4; ++u)
+        r[u] = rows_of(4 * tile + u, __builtin_amdgcn_readlane(page, 16 * u));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const char* p = static_cast<const char*>(a.c.v) + r[u] * D * ES;
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+          v.r[u][k] = *reinterpret_cast<const Reg*>(p + (lane + 64 * k) * 8 * ES);
+      }
+      if constexpr (HALF) {                 // lanes 32 .. 63: the same values, two groups on
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const char* p = static_cast<const char*>(a.c.v) + (lane < 32 ? r[u] : r[u + 2]) * D * ES;
+          v.h[u] = *reinterpret_cast<const Reg*>(p + ((lane & 31) + 64 * C) * 8 * ES);
+        }
+      }
       if constexpr (I8) {
+        const int64_t rs = g == 0 ? r[0] : g == 1 ? r[1] : g == 2 ? r[2] : r[3];
 #pragma unroll
         for (int w = 0; w < NW; ++w)
-          v.s[w] = a.c.vs[r * NB + 16 * w + (2 * w + 1 < NB ? n : (n & 7))];
+          v.s[w] = a.c.vs[rs * NB + 16 * w + (2 * w + 1 < NB ? n : (n & 7))];
       }
     };
 
@@ -284,17 +296,119 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
         pv = page_of(4 * (tile0 + u) + g);
       }
     };
+    next_pages(t);
+
+    // ---- the query rows: row n of this wave's tile, as two halves, scaled by 2^(14 - ex)
+    const int row = rg * ROWS + wr * WROWS + n;
+    const bool row_ok = n < WROWS && row < rows_all;
+    const int row_t = row_ok ? row / a.group : 0;
+    const int row_h = kvh * a.group + (row_ok ? row - row_t * a.group : 0);
+    const int row_pos = len - a.T + row_t;                  // this row's position
+    float qx[NB][8];
+    {
+      const float* qp = a.q + ((int64_t)b * a.T + row_t) * a.q_stride + (int64_t)row_h * D + 8 * g;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const float4 u = row_ok ? *reinterpret_cast<const float4*>(qp + 32 * k)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 v = row_ok ? *reinterpret_cast<const float4*>(qp + 32 * k + 4)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+        qx[k][0] = u.x; qx[k][1] = u.y; qx[k][2] = u.z; qx[k][3] = u.w;
+        qx[k][4] = v.x; qx[k][5] = v.y; qx[k][6] = v.z; qx[k][7] = v.w;
+      }
+    }
     if (t < t1) {
-      next_pages(t);
       load_k(tile0 + t, pk, pv);
       load_v(va, tile0 + t, pv);
       next_pages(t + WT);
     }
+    half8v qh[NB], ql[NB];
+    float c;                                                // score -> base 2, unscaled
+    {
+      float big = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(qx[k][i]));
+      big = max_over_groups(big);
+      // 2^(14 - ex) > 2^13 / big, from the exponent's bits; not for 0, infinity
+      const int e = (int)(__float_as_uint(big) >> 23);
+      const int ex = e == 0 ? (big > 0.0f ? -100 : 0) : e == 255 ? 0 : max(e - 126, -100);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) qx[k][i] *= up;
+        split8(qx[k], qh[k], ql[k]);
+      }
+      c = a.scale * 1.44269504088896340736f * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+    }
+
+    // ---- the stream of tiles
+    float4v o[CA][Q];                       // lane: value 64 i + lane of four query rows
+#pragma unroll
+    for (int i = 0; i < CA; ++i)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) o[i][q] = float4v{0.f, 0.f, 0.f, 0.f};
+    float m = kLowest, l = 0.0f;
+
+    // sum += V^T W of a tile, W in `weights` (transposed through LDS: a lane needs the
+    // weights of row lane % 4 for one token, and holds one value of eight tokens)
+    auto add_products = [&](const Values& v, float4v (&sum)[CA][Q], auto scaled_by_s) {
+      const float* w0 = &weights[wave][lane & 3][(lane >> 2) & 7];
+      unrolled<0, 4>([&](auto uc) {
+        constexpr int u = uc;
+        float w[Q], s[CA];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) w[q] = w0[(4 * q) * 36 + 8 * u];
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+          s[k] = scaled_by_s ? lane_of(v.s[k], 16 * u + 8 * (lane >> 5) + ((lane >> 2) & 7)) : 1.0f;
+        unrolled<0, 8>([&](auto jc) {
+          constexpr int j = jc;
+#pragma unroll
+          for (int k = 0; k < C; ++k) {
+            const float x = value_of<j>(v.r[u][k]);
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+              sum[k][q] = mfma4<j>(scaled_by_s ? w[q] * s[k] : w[q], x, sum[k][q]);
+          }
+        });
+      });
+      if constexpr (HALF) {
+        const float* wh = w0 + 16 * (lane >> 5);
+        unrolled<0, 2>([&](auto uc) {
+          constexpr int u = uc;
+          const float s =
+              scaled_by_s ? lane_of(v.s[NW - 1], 16 * (u + 2 * (lane >> 5)) + ((lane >> 2) & 7))
+                          : 1.0f;
+          float w[Q];
+#pragma unroll
+          for (int q = 0; q < Q; ++q) w[q] = wh[(4 * q) * 36 + 8 * u] * s;
+          unrolled<0, 8>([&](auto jc) {
+            constexpr int j = jc;
+            const float x = value_of<j>(v.h[u]);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) sum[C][q] = mfma4<j>(w[q], x, sum[C][q]);
+          });
+        });
+      }
+    };
+    auto put_weights = [&](const float (&p)[8]) {
+      wave_fence();
+      if (n < WROWS) {
+        float4* w = reinterpret_cast<float4*>(&weights[wave][n][8 * g]);
+        w[0] = make_float4(p[0], p[1], p[2], p[3]);
+        w[1] = make_float4(p[4], p[5], p[6], p[7]);
+      }
+      wave_fence();
+    };
+
     // One tile: its values lie in `v`, the next tile's go to `next`.
     auto step = [&](Values& v, Values& next) {
       const int tile = tile0 + t;
       const bool more = t + WT < t1;
-      // scores: s[4 s + i] of token 8 g + 4 s + i
+      // scores: x[4 s + i] of token 8 g + 4 s + i
       float x[8];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -345,7 +459,7 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
         if (a.err) *a.err = 1;
       }
       if (edge) {
-        const int64_t from = a.window > 0 ? row_pos - a.window + 1 : 0;
+        const int from = a.window > 0 ? (int)max((int64_t)-1, row_pos - a.window) + 1 : 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (pos0 + j > row_pos || pos0 + j < from) x[j] = -INFINITY;
@@ -368,12 +482,14 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
               if ((uint32_t)(odd[k >> 1] >> (16 * g + 8 * (k & 1))) & seen) lost |= 1u << k;
             lost |= __shfl_xor(lost, 16, 64);
             lost |= __shfl_xor(lost, 32, 64);
+            unrolled<0, WROWS>([&](auto rc) {
+              constexpr int r = rc;
+              const uint32_t of_row = __float_as_uint(row_bcast<r>(__uint_as_float(lost)));
 #pragma unroll
-            for (int k = 0; k < NB; ++k)
-              if (lost >> k & 1) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[2 * k + i / 4][i % 4] = __builtin_nanf("");
-              }
+              for (int k = 0; k < CA; ++k)
+                if (of_row >> (2 * k + (k < C ? lane >> 5 : 0)) & 1)
+                  o[k][r >> 2][r & 3] = __builtin_nanf("");
+            });
 #pragma unroll
             for (int w = 0; w < NW; ++w)
               if (!(fabsf(v.s[w]) < INFINITY)) v.s[w] = 0.0f;
@@ -390,10 +506,12 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
         const float fix = __builtin_amdgcn_exp2f(m - m_new);
         m = m_new;
         l *= fix;
+        unrolled<0, WROWS>([&](auto rc) {
+          constexpr int r = rc;
+          const float f = row_bcast<r>(fix);
 #pragma unroll
-        for (int i = 0; i < 2 * NB; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][e] *= fix;
+          for (int k = 0; k < CA; ++k) o[k][r >> 2][r & 3] *= f;
+        });
       }
       float p[8];
 #pragma unroll
@@ -402,65 +520,86 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
         l += p[j];
       }
 
-      if constexpr (I8) {
-        unrolled<0, NB>([&](auto kc) {
-          constexpr int k = kc;
-          const uint4 c4 = v.r[k];
-          unrolled<0, 8>([&](auto jc) {
-            constexpr int j = jc;
-            const float w = row_bcast<(k & 1) * 8 + j>(v.s[k >> 1]) * p[j];
-            o[2 * k] = mfma4(code_of<j & 3>(j < 4 ? c4.x : c4.y), w, o[2 * k]);
-            o[2 * k + 1] = mfma4(code_of<j & 3>(j < 4 ? c4.z : c4.w), w, o[2 * k + 1]);
-          });
-        });
-      } else {
+      if constexpr (!I8) {
         if (edge) {
           // Hidden tokens may hold infinities or NaN, which a weight of 0 does not
           // cancel.  Where a tile holds any, they are taken out, and each row that
           // does see one gets it back: the number of seen infinities of either sign
           // (NaN counts as both) comes from the matrix core.
           bool odd = false;
-#pragma unroll
-          for (int k = 0; k < 2 * NB; ++k) {
-            const uint32_t w[4] = {v.r[k].x, v.r[k].y, v.r[k].z, v.r[k].w};
+          auto look = [&](const Reg& r) {
+            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               odd |= (w[i] & 0x7C00u) == 0x7C00u || (w[i] & 0x7C000000u) == 0x7C000000u;
-          }
-          if (__any(odd)) {
-            half8v seen;
+          };
+          auto each = [&](auto&& f) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) seen[j] = (_Float16)(x[j] == -INFINITY ? 0.0f : 1.0f);
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int k = 0; k < 2 * NB; ++k) {
-              half8v f8 = halves_of(v.r[k]), up, dn;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float f = (float)f8[j];
-                up[j] = (_Float16)(f < INFINITY ? 0.0f : 1.0f);
-                dn[j] = (_Float16)(f > -INFINITY ? 0.0f : 1.0f);
-                if (!(fabsf(f) < INFINITY)) f8[j] = (_Float16)0.0f;
-              }
-              const float4v zero = {0.f, 0.f, 0.f, 0.f};
-              const float4v nu = mfma(up, seen, zero), nd = mfma(dn, seen, zero);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (nu[i] > 0.0f) o[k][i] += INFINITY;
-                if (nd[i] > 0.0f) o[k][i] -= INFINITY;
-              }
-              union { half8v v; uint4 u; } back;
-              back.v = f8;
-              v.r[k] = back.u;
+              for (int k = 0; k < C; ++k) f(v.r[u][k], u, k);
+            if constexpr (HALF) {
+              f(v.h[0], 0, C);
+              f(v.h[1], 1, C);
             }
+          };
+          each([&](Reg& r, int, int) { look(r); });
+          if (__any(odd)) {
+            float seen[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) seen[j] = x[j] == -INFINITY ? 0.0f : 1.0f;
+            put_weights(seen);
+            // the tile with every half replaced by 1 where `what` holds, else 0
+            auto marks = [&](auto&& what) {
+              Values z = v;
+              auto mark = [&](Reg& r) {
+                union { Reg u; half8v h; } b_;
+                b_.u = r;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) b_.h[j] = (_Float16)(what((float)b_.h[j]) ? 1.0f : 0.0f);
+                r = b_.u;
+              };
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int k = 0; k < C; ++k) mark(z.r[u][k]);
+              if constexpr (HALF) {
+                mark(z.h[0]);
+                mark(z.h[1]);
+              }
+              return z;
+            };
+#pragma unroll
+            for (int sign = 0; sign < 2; ++sign) {
+              const Values z = sign ? marks([](float f) { return !(f > -INFINITY); })
+                                    : marks([](float f) { return !(f < INFINITY); });
+              float4v count[CA][Q];
+#pragma unroll
+              for (int k = 0; k < CA; ++k)
+#pragma unroll
+                for (int q = 0; q < Q; ++q) count[k][q] = float4v{0.f, 0.f, 0.f, 0.f};
+              add_products(z, count, std::false_type{});
+#pragma unroll
+              for (int k = 0; k < CA; ++k)
+#pragma unroll
+                for (int q = 0; q < Q; ++q)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    if (count[k][q][i] > 0.0f) o[k][q][i] += sign ? -INFINITY : INFINITY;
+            }
+            each([&](Reg& r, int, int) {
+              union { Reg u; half8v h; } b_;
+              b_.u = r;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (!(fabsf((float)b_.h[j]) < INFINITY)) b_.h[j] = (_Float16)0.0f;
+              r = b_.u;
+            });
           }
-        }
-#pragma unroll
-        for (int k = 0; k < 2 * NB; ++k) {
-          const half8v f8 = halves_of(v.r[k]);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[k] = mfma4((float)f8[j], p[j], o[k]);
         }
       }
+      put_weights(p);
+      add_products(v, o, std::bool_constant<I8>{});
       t += WT;
     };
     while (t < t1) {
@@ -470,25 +609,30 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
 
     // ---- the waves' sums together, then out: finished, or into this share's slot
     l = sum_over_groups(l);
-    if (lane < 16) wave_ml[wave][lane] = make_float2(m, l);
+    if (lane < WROWS) wave_ml[wave][lane] = make_float2(m, l);
     __syncthreads();
     float m_all = m;
+    if (n < WROWS) {
 #pragma unroll
-    for (int w = 0; w < WT; ++w) m_all = fmaxf(m_all, wave_ml[w * RW + wr][n].x);
+      for (int w = 0; w < WT; ++w) m_all = fmaxf(m_all, wave_ml[w * RW + wr][n].x);
+    }
     const float fix = __builtin_amdgcn_exp2f(m - m_all);
-    unrolled<0, 2 * NB>([&](auto kc) {
-      constexpr int k = kc;
+    unrolled<0, WROWS>([&](auto rc) {
+      constexpr int r = rc;
+      const float f = row_bcast<r>(fix);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = I8 ? 32 * (k >> 1) + 2 * (4 * g + i) + (k & 1) : 16 * k + 4 * g + i;
-        sums[wave][n][d] = o[k][i] * fix;
+      for (int k = 0; k < C; ++k) sums[wave][r][64 * k + lane] = o[k][r >> 2][r & 3] * f;
+      if constexpr (HALF) {
+        const float h = o[C][r >> 2][r & 3] * f;
+        const float both = h + __shfl_xor(h, 32, 64);
+        if (lane < 32) sums[wave][r][64 * C + lane] = both;
       }
     });
     __syncthreads();
     const int rows_here = min(ROWS, rows_all - rg * ROWS);
     for (int e = tid; e < rows_here * (D / 4); e += kAttnThreads) {
       const int r = e / (D / 4), d = 4 * (e - r * (D / 4));
-      const int tile_r = r >> 4, rn = r & 15;
+      const int tile_r = r / WROWS, rn = r % WROWS;
       float mm = kLowest, ll = 0.0f;
 #pragma unroll
       for (int w = 0; w < WT; ++w) mm = fmaxf(mm, wave_ml[w * RW + tile_r][rn].x);
@@ -518,18 +662,20 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
 }
 
 template <bool I8, int NB>
-hipError_t launch_attn(const AttnArgs& a, int rw, int grid, hipStream_t stream) {
-  const auto kernel = rw == 1 ? paged_attn_kernel<I8, NB, 1>
-                      : rw == 2 ? paged_attn_kernel<I8, NB, 2>
-                                : paged_attn_kernel<I8, NB, 4>;
+hipError_t launch_attn(const AttnArgs& a, int rows, int grid, hipStream_t stream) {
+  const auto kernel = rows <= 4    ? paged_attn_kernel<I8, NB, 1, 1>
+                      : rows <= 8  ? paged_attn_kernel<I8, NB, 2, 1>
+                      : rows <= 16 ? paged_attn_kernel<I8, NB, 4, 1>
+                      : rows <= 32 ? paged_attn_kernel<I8, NB, 4, 2>
+                                   : paged_attn_kernel<I8, NB, 4, 4>;
   hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(kAttnThreads), 0, stream, a);
   return hipGetLastError();
 }
 
 template <int NB>
-hipError_t launch_attn_nb(const AttnArgs& a, bool i8, int rw, int grid, hipStream_t stream) {
-  return i8 ? launch_attn<true, NB>(a, rw, grid, stream)
-            : launch_attn<false, NB>(a, rw, grid, stream);
+hipError_t launch_attn_nb(const AttnArgs& a, bool i8, int rows, int grid, hipStream_t stream) {
+  return i8 ? launch_attn<true, NB>(a, rows, grid, stream)
+            : launch_attn<false, NB>(a, rows, grid, stream);
 }
 
 }  // namespace rfp2
