@@ -51,8 +51,16 @@
 namespace rfp2 {
 
 constexpr int kAttnThreads = 256;
-constexpr int kAttnGroups = 512;          // workgroups (shares) of a launch at most
+constexpr int kAttnCus = 256;             // compute units that shares are made for
+constexpr int kAttnGroups = 3 * kAttnCus; // workgroups (shares) of a launch at most
 constexpr int kAttnMinTiles = 4;          // tiles of a share at least
+
+// Waves a SIMD, and so workgroups a compute unit, that a variant's registers allow
+// without spilling (as the compiler reported them; q: groups of four query rows).
+constexpr int attn_waves(bool i8, int nb, int q) {
+  if (nb <= 4) return i8 && q <= 2 ? 3 : 2;
+  return (i8 ? nb + q / 2 <= 8 : nb == 5 && q == 1) ? 2 : 1;
+}
 
 struct AttnArgs {
   KvView c;

@@ -140,8 +140,10 @@ hipError_t launch_paged_attn(const KvView& c, bool i8, const float* q, int64_t B
   // no more workgroups than shares of the longest lengths the page table allows
   const int64_t tiles = ((((int64_t)c.max_pages << c.page_shift) + 31) / 32 + 1) * B * c.heads *
                         a.row_groups;
-  const int grid = (int)std::min<int64_t>(kAttnGroups, (tiles + kAttnMinTiles - 1) / kAttnMinTiles);
-  const int nb = c.dim / 32;
+  const int nb = c.dim / 32, quads = rows <= 4 ? 1 : rows <= 8 ? 2 : 4;
+  const int grid = (int)std::min<int64_t>(kAttnCus * attn_waves(i8, nb, quads),
+                                          std::max((tiles + kAttnMinTiles - 1) / kAttnMinTiles,
+                                                   (int64_t)c.heads * a.row_groups));
   const auto launch = nb <= 2   ? launch_paged_attn_12
                       : nb <= 4 ? launch_paged_attn_34
                       : nb <= 6 ? launch_paged_attn_56

@@ -116,12 +116,19 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// The same number, computed here: what a lane derives from it (offsets, masks) is not
+// carried in registers from further up.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 constexpr float kLowest = -3.0e38f;        // the running maximum before any score
 constexpr float kSlack = 8.0f;             // weights may grow to 2^8 before sums are rescaled
 
 // Q: groups of four query rows of a wave (1, 2 or 4); RW as described in paged_attn.h.
 template <bool I8, int NB, int Q, int RW>
-__global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_kernel(
+__global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_attn_kernel(
     const AttnArgs a) {
   constexpr int D = 32 * NB, WT = 4 / RW, WROWS = 4 * Q, ROWS = WROWS * RW, NW = (NB + 1) / 2;
   constexpr int C = NB / 2;                 // whole chunks of 64 values
@@ -136,14 +143,13 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
   __shared__ float sums[4][WROWS][D + 4];
   __shared__ float weights[4][WROWS][36];
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wr = wave % RW, wt = wave / RW;
-  const int n = lane & 15, g = lane >> 4;
   const int64_t cap = (int64_t)a.c.max_pages << a.c.page_shift;
 
   // ---- the line of tiles: cum[b] = tiles of one item of sequences before b
   {
+    const int tid = threadIdx.x, lane = tid & 63;
     uint32_t nt[4], mine = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -184,12 +190,26 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
     __syncthreads();
   }
   const int items = a.c.heads * a.row_groups;
-  const int64_t total = (int64_t)cum[a.B] * items;
-  const int64_t share =
-      max((int64_t)kAttnMinTiles, divided(total + (int64_t)gridDim.x - 1, (int64_t)gridDim.x));
+  // Shares: equal parts of the line.  One sequence's items are cut alike instead, into as
+  // many parts as there are workgroups for, so that no workgroup works on two items.
+  const bool alike = a.B == 1 && items <= (int)gridDim.x;
+  uint32_t line1 = cum[1];
+  int64_t share;
+  if (alike) {
+    const uint32_t parts = max(1u, min(gridDim.x / (uint32_t)items,
+                                       (line1 + kAttnMinTiles - 1) / kAttnMinTiles));
+    const uint32_t len1 = max(1u, (line1 + parts - 1) / parts);
+    line1 = (line1 + len1 - 1) / len1 * len1;
+    share = len1;
+  } else {
+    share = max((int64_t)kAttnMinTiles,
+                divided((int64_t)cum[a.B] * items + gridDim.x - 1, (int64_t)gridDim.x));
+  }
+  auto line = [&](int i) { return a.B == 1 && i == 1 ? line1 : cum[i]; };
+  const int64_t total = (int64_t)line(a.B) * items;
   if (blockIdx.x == 0) {
-    if (tid == 0) a.plan[0] = share;
-    for (int b = tid; b <= a.B; b += kAttnThreads) a.cum[b] = cum[b];
+    if (threadIdx.x == 0) a.plan[0] = share;
+    for (int b = threadIdx.x; b <= a.B; b += kAttnThreads) a.cum[b] = line(b);
   }
   const int64_t first_unit = blockIdx.x * share;
   const int64_t end_unit = min(total, first_unit + share);
@@ -204,15 +224,17 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
   }
 
   for (int64_t unit = first_unit; unit < end_unit;) {
-    while (unit >= (int64_t)cum[b + 1] * items) ++b;        // sequences without tiles
-    const int64_t nt = cum[b + 1] - cum[b];
+    while (unit >= (int64_t)line(b + 1) * items) ++b;       // sequences without tiles
+    int64_t nt = line(b + 1) - cum[b];
     const int64_t in_seq = unit - (int64_t)cum[b] * items;
     const int item = (int)divided(in_seq, nt);
     const int t0 = (int)(in_seq - item * nt);
-    const int t1 = (int)min(nt, t0 + (end_unit - unit));
-    const bool whole = t0 == 0 && t1 == nt;
     const int slot = unit == first_unit ? 0 : 1;
-    unit += t1 - t0;
+    const int64_t here_ = min(nt - t0, end_unit - unit);
+    unit += here_;
+    if (alike) nt = cum[1];                                  // without the rounding up
+    const int t1 = (int)min(nt, t0 + here_);
+    const bool whole = t0 == 0 && t1 == nt;
 
     const int kvh = item / a.row_groups, rg = item - kvh * a.row_groups;
     const int rows_all = a.T * a.group;
@@ -220,6 +242,8 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
     const int lo = a.window > 0 ? (int)max((int64_t)0, len - a.T - a.window + 1) : 0;
     const int tile0 = lo >> 5;
     const int group_lo = lo >> 3, group_hi = (len - 1) >> 3;
+
+    const int lane = here(threadIdx.x) & 63, n = lane & 15, g = lane >> 4;
 
     // ---- the cache's tiles
     struct Keys {                           // a tile's keys and their scales
@@ -299,14 +323,15 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
     next_pages(t);
 
     // ---- the query rows: row n of this wave's tile, as two halves, scaled by 2^(14 - ex)
-    const int row = rg * ROWS + wr * WROWS + n;
-    const bool row_ok = n < WROWS && row < rows_all;
+    const int lane_q = here(threadIdx.x) & 63, nq = lane_q & 15, gq = lane_q >> 4;
+    const int row = rg * ROWS + wr * WROWS + nq;
+    const bool row_ok = nq < WROWS && row < rows_all;
     const int row_t = row_ok ? row / a.group : 0;
     const int row_h = kvh * a.group + (row_ok ? row - row_t * a.group : 0);
     const int row_pos = len - a.T + row_t;                  // this row's position
     float qx[NB][8];
     {
-      const float* qp = a.q + ((int64_t)b * a.T + row_t) * a.q_stride + (int64_t)row_h * D + 8 * g;
+      const float* qp = a.q + ((int64_t)b * a.T + row_t) * a.q_stride + (int64_t)row_h * D + 8 * gq;
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         const float4 u = row_ok ? *reinterpret_cast<const float4*>(qp + 32 * k)
@@ -354,7 +379,7 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
 
     // sum += V^T W of a tile, W in `weights` (transposed through LDS: a lane needs the
     // weights of row lane % 4 for one token, and holds one value of eight tokens)
-    auto add_products = [&](const Values& v, float4v (&sum)[CA][Q], auto scaled_by_s) {
+    auto add_products = [&](const Values& v, float4v (&sum)[CA][Q], auto scaled_by_s, auto&& of) {
       const float* w0 = &weights[wave][lane & 3][(lane >> 2) & 7];
       unrolled<0, 4>([&](auto uc) {
         constexpr int u = uc;
@@ -368,7 +393,7 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
           constexpr int j = jc;
 #pragma unroll
           for (int k = 0; k < C; ++k) {
-            const float x = value_of<j>(v.r[u][k]);
+            const float x = of(value_of<j>(v.r[u][k]));
 #pragma unroll
             for (int q = 0; q < Q; ++q)
               sum[k][q] = mfma4<j>(scaled_by_s ? w[q] * s[k] : w[q], x, sum[k][q]);
@@ -387,7 +412,7 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
           for (int q = 0; q < Q; ++q) w[q] = wh[(4 * q) * 36 + 8 * u] * s;
           unrolled<0, 8>([&](auto jc) {
             constexpr int j = jc;
-            const float x = value_of<j>(v.h[u]);
+            const float x = of(value_of<j>(v.h[u]));
 #pragma unroll
             for (int q = 0; q < Q; ++q) sum[C][q] = mfma4<j>(w[q], x, sum[C][q]);
           });
@@ -440,7 +465,10 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[4 * s + i] = acc[i] * c;
+        for (int i = 0; i < 4; ++i) {
+          x[4 * s + i] = acc[i] * c;
+          asm volatile("" : "+v"(x[4 * s + i]));   // not put off until after the loads
+        }
       }
       // the next tile's keys and values are on their way while this one is worked on
       if (more) {
@@ -474,12 +502,13 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
 #pragma unroll
           for (int w = 0; w < NW; ++w) any_odd |= odd[w] = __ballot(!(fabsf(v.s[w]) < INFINITY));
           if (any_odd) {
+            const int lane_o = here(threadIdx.x) & 63, g_o = lane_o >> 4;
             uint32_t seen = 0, lost = 0;                     // tokens; blocks
 #pragma unroll
             for (int j = 0; j < 8; ++j) seen |= (x[j] != -INFINITY ? 1u : 0u) << j;
 #pragma unroll
             for (int k = 0; k < NB; ++k)
-              if ((uint32_t)(odd[k >> 1] >> (16 * g + 8 * (k & 1))) & seen) lost |= 1u << k;
+              if ((uint32_t)(odd[k >> 1] >> (16 * g_o + 8 * (k & 1))) & seen) lost |= 1u << k;
             lost |= __shfl_xor(lost, 16, 64);
             lost |= __shfl_xor(lost, 32, 64);
             unrolled<0, WROWS>([&](auto rc) {
@@ -487,7 +516,7 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
               const uint32_t of_row = __float_as_uint(row_bcast<r>(__uint_as_float(lost)));
 #pragma unroll
               for (int k = 0; k < CA; ++k)
-                if (of_row >> (2 * k + (k < C ? lane >> 5 : 0)) & 1)
+                if (of_row >> (2 * k + (k < C ? lane_o >> 5 : 0)) & 1)
                   o[k][r >> 2][r & 3] = __builtin_nanf("");
             });
 #pragma unroll
@@ -549,44 +578,23 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
 #pragma unroll
             for (int j = 0; j < 8; ++j) seen[j] = x[j] == -INFINITY ? 0.0f : 1.0f;
             put_weights(seen);
-            // the tile with every half replaced by 1 where `what` holds, else 0
-            auto marks = [&](auto&& what) {
-              Values z = v;
-              auto mark = [&](Reg& r) {
-                union { Reg u; half8v h; } b_;
-                b_.u = r;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) b_.h[j] = (_Float16)(what((float)b_.h[j]) ? 1.0f : 0.0f);
-                r = b_.u;
-              };
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int k = 0; k < C; ++k) mark(z.r[u][k]);
-              if constexpr (HALF) {
-                mark(z.h[0]);
-                mark(z.h[1]);
-              }
-              return z;
-            };
-#pragma unroll
-            for (int sign = 0; sign < 2; ++sign) {
-              const Values z = sign ? marks([](float f) { return !(f > -INFINITY); })
-                                    : marks([](float f) { return !(f < INFINITY); });
-              float4v count[CA][Q];
+            auto count = [&](float inf, auto&& of) {
+              float4v seen_of[CA][Q];
 #pragma unroll
               for (int k = 0; k < CA; ++k)
 #pragma unroll
-                for (int q = 0; q < Q; ++q) count[k][q] = float4v{0.f, 0.f, 0.f, 0.f};
-              add_products(z, count, std::false_type{});
+                for (int q = 0; q < Q; ++q) seen_of[k][q] = float4v{0.f, 0.f, 0.f, 0.f};
+              add_products(v, seen_of, std::false_type{}, of);
 #pragma unroll
               for (int k = 0; k < CA; ++k)
 #pragma unroll
                 for (int q = 0; q < Q; ++q)
 #pragma unroll
                   for (int i = 0; i < 4; ++i)
-                    if (count[k][q][i] > 0.0f) o[k][q][i] += sign ? -INFINITY : INFINITY;
-            }
+                    if (seen_of[k][q][i] > 0.0f) o[k][q][i] += inf;
+            };
+            count(INFINITY, [](float f) { return f < INFINITY ? 0.0f : 1.0f; });
+            count(-INFINITY, [](float f) { return f > -INFINITY ? 0.0f : 1.0f; });
             each([&](Reg& r, int, int) {
               union { Reg u; half8v h; } b_;
               b_.u = r;
@@ -599,7 +607,7 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
         }
       }
       put_weights(p);
-      add_products(v, o, std::bool_constant<I8>{});
+      add_products(v, o, std::bool_constant<I8>{}, [](float f) { return f; });
       t += WT;
     };
     while (t < t1) {
@@ -608,29 +616,30 @@ __global__ __launch_bounds__(kAttnThreads, (NB <= 4 ? 2 : 1)) void paged_attn_ke
     }
 
     // ---- the waves' sums together, then out: finished, or into this share's slot
+    const int tid_ = here(threadIdx.x), lane_ = tid_ & 63, n_ = lane_ & 15;
     l = sum_over_groups(l);
-    if (lane < WROWS) wave_ml[wave][lane] = make_float2(m, l);
+    if (lane_ < WROWS) wave_ml[wave][lane_] = make_float2(m, l);
     __syncthreads();
     float m_all = m;
-    if (n < WROWS) {
+    if (n_ < WROWS) {
 #pragma unroll
-      for (int w = 0; w < WT; ++w) m_all = fmaxf(m_all, wave_ml[w * RW + wr][n].x);
+      for (int w = 0; w < WT; ++w) m_all = fmaxf(m_all, wave_ml[w * RW + wr][n_].x);
     }
     const float fix = __builtin_amdgcn_exp2f(m - m_all);
     unrolled<0, WROWS>([&](auto rc) {
       constexpr int r = rc;
       const float f = row_bcast<r>(fix);
 #pragma unroll
-      for (int k = 0; k < C; ++k) sums[wave][r][64 * k + lane] = o[k][r >> 2][r & 3] * f;
+      for (int k = 0; k < C; ++k) sums[wave][r][64 * k + lane_] = o[k][r >> 2][r & 3] * f;
       if constexpr (HALF) {
         const float h = o[C][r >> 2][r & 3] * f;
         const float both = h + __shfl_xor(h, 32, 64);
-        if (lane < 32) sums[wave][r][64 * C + lane] = both;
+        if (lane_ < 32) sums[wave][r][64 * C + lane_] = both;
       }
     });
     __syncthreads();
     const int rows_here = min(ROWS, rows_all - rg * ROWS);
-    for (int e = tid; e < rows_here * (D / 4); e += kAttnThreads) {
+    for (int e = tid_; e < rows_here * (D / 4); e += kAttnThreads) {
       const int r = e / (D / 4), d = 4 * (e - r * (D / 4));
       const int tile_r = r / WROWS, rn = r % WROWS;
       float mm = kLowest, ll = 0.0f;
