@@ -51,15 +51,17 @@
 namespace rfp2 {
 
 constexpr int kAttnThreads = 256;
+constexpr int kJoinThreads = 256;
 constexpr int kAttnCus = 256;             // compute units that shares are made for
 constexpr int kAttnGroups = 3 * kAttnCus; // workgroups (shares) of a launch at most
+constexpr int kAttnItemStart = 8;         // tiles in whose time a workgroup starts on an item
 constexpr int kAttnMinTiles = 4;          // tiles of a share at least
 
-// Waves a SIMD, and so workgroups a compute unit, that a variant's registers allow
-// without spilling (as the compiler reported them; q: groups of four query rows).
+// Waves a SIMD that a variant's registers allow without spilling (as the compiler
+// reported them; nb: blocks of 32 values of a head, q: groups of four query rows).
 constexpr int attn_waves(bool i8, int nb, int q) {
-  if (nb <= 4) return i8 && q <= 2 ? 3 : 2;
-  return (i8 ? nb + q / 2 <= 8 : nb == 5 && q == 1) ? 2 : 1;
+  if (i8) return nb <= 4 || (nb <= 6 && q == 1) ? 3 : nb <= 7 || q <= 2 ? 2 : 1;
+  return nb <= 4 ? (q == 1 ? 3 : 2) : (nb <= 6 && q <= 2) || q == 1 ? 2 : 1;
 }
 
 struct AttnArgs {
@@ -77,7 +79,7 @@ struct AttnArgs {
   int32_t slot_rows;                      // rows of a slot of the workspace
   // workspace
   int64_t* plan;                          // [0] tiles a share
-  uint32_t* cum;                          // [B + 1] tiles of one item of the sequences before
+  uint32_t* cum;                          // [B + 1] length of one item of the sequences before
   float2* ml;                             // [groups][2][slot_rows] maximum (base 2) and sum
   float* part;                            // [groups][2][slot_rows][D] sums
 };

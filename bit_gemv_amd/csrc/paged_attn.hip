@@ -8,7 +8,7 @@ namespace {
 
 // Query rows of an item: what the kernel variant that launch_attn picks takes at once.
 int item_rows(int64_t rows) {
-  return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -32,22 +32,23 @@ Layout layout(int64_t dim, int64_t B, int64_t rows) {
 // row's values, the rest of the workgroup other parts.  Also writes the rows
 // that no tile belongs to: sequences without tokens (zeros) or with an
 // impossible length (NaN).
-__global__ __launch_bounds__(kAttnThreads) void paged_attn_join_kernel(const AttnArgs a,
+__global__ __launch_bounds__(kJoinThreads) void paged_attn_join_kernel(const AttnArgs a,
                                                                        int rows_of_item) {
-  __shared__ float red[kAttnThreads / 64];
-  __shared__ float4 acc[kAttnThreads];
-  __shared__ float accl[kAttnThreads];
+  __shared__ float red[kJoinThreads / 64];
+  __shared__ float4 acc[kJoinThreads];
+  __shared__ float accl[kJoinThreads];
   const int D = a.c.dim, tid = threadIdx.x;
   const int64_t row = blockIdx.x;                   // (b * T + t) * H + h
   const int h = (int)(row % a.H);
   const int64_t bt = row / a.H;
   const int t = (int)(bt % a.T), b = (int)(bt / a.T);
-  const int64_t nt = a.cum[b + 1] - a.cum[b];
+  const int64_t length = a.cum[b + 1] - a.cum[b];   // of an item of this sequence
+  const int start = a.B == 1 ? 0 : kAttnItemStart;
   const int lanes = D >> 2;                         // 8 .. 64
-  const int lane = tid % lanes, group = tid / lanes, groups = kAttnThreads / lanes;
+  const int lane = tid % lanes, group = tid / lanes, groups = kJoinThreads / lanes;
   const bool active = group < groups;
   float4* out = reinterpret_cast<float4*>(a.y + row * D);
-  if (nt == 0) {
+  if (length == 0) {
     const float v = a.lens[b] > 0 ? __builtin_nanf("") : 0.0f;
     if (tid < lanes) out[tid] = make_float4(v, v, v, v);
     return;
@@ -57,8 +58,9 @@ __global__ __launch_bounds__(kAttnThreads) void paged_attn_join_kernel(const Att
   const int rg = r / rows_of_item;
   const int64_t share = a.plan[0];
   const int64_t items = (int64_t)a.c.heads * a.row_groups;
-  const int64_t first = (int64_t)a.cum[b] * items + (int64_t)(kvh * a.row_groups + rg) * nt;
-  const int64_t w0 = first / share, w1 = (first + nt - 1) / share;
+  const int64_t first =
+      (int64_t)a.cum[b] * items + (int64_t)(kvh * a.row_groups + rg) * length + start;
+  const int64_t w0 = first / share, w1 = (first + length - start - 1) / share;
   if (w0 == w1) return;                             // written by its one workgroup
   const int parts = (int)(w1 - w0 + 1);
   // part i is slot 0 of workgroup w0 + i, but for a first one that starts inside its share
@@ -69,7 +71,7 @@ __global__ __launch_bounds__(kAttnThreads) void paged_attn_join_kernel(const Att
     return (2 * w + slot) * a.slot_rows + r_in;
   };
   float m = -INFINITY;
-  for (int i = tid; i < parts; i += kAttnThreads) m = fmaxf(m, a.ml[at(i)].x);
+  for (int i = tid; i < parts; i += kJoinThreads) m = fmaxf(m, a.ml[at(i)].x);
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   if ((tid & 63) == 0) red[tid >> 6] = m;
   __syncthreads();
@@ -140,7 +142,7 @@ hipError_t launch_paged_attn(const KvView& c, bool i8, const float* q, int64_t B
   // no more workgroups than shares of the longest lengths the page table allows
   const int64_t tiles = ((((int64_t)c.max_pages << c.page_shift) + 31) / 32 + 1) * B * c.heads *
                         a.row_groups;
-  const int nb = c.dim / 32, quads = rows <= 4 ? 1 : rows <= 8 ? 2 : 4;
+  const int nb = c.dim / 32, quads = rows <= 4 ? 1 : rows <= 8 ? 2 : ir == 48 ? 3 : 4;
   const int grid = (int)std::min<int64_t>(kAttnCus * attn_waves(i8, nb, quads),
                                           std::max((tiles + kAttnMinTiles - 1) / kAttnMinTiles,
                                                    (int64_t)c.heads * a.row_groups));
@@ -151,7 +153,7 @@ hipError_t launch_paged_attn(const KvView& c, bool i8, const float* q, int64_t B
   hipError_t e = launch(a, i8, nb, (int)std::min<int64_t>(rows, 64), grid, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(paged_attn_join_kernel, dim3((uint32_t)(B * new_tokens * H)),
-                     dim3(kAttnThreads), 0, stream, a, ir);
+                     dim3(kJoinThreads), 0, stream, a, ir);
   return hipGetLastError();
 }
 

@@ -126,34 +126,46 @@ __device__ __forceinline__ int here(int x) {
 constexpr float kLowest = -3.0e38f;        // the running maximum before any score
 constexpr float kSlack = 8.0f;             // weights may grow to 2^8 before sums are rescaled
 
-// Q: groups of four query rows of a wave (1, 2 or 4); RW as described in paged_attn.h.
+// Q: groups of four query rows of a wave (1 to 4); RW as described in paged_attn.h.
 template <bool I8, int NB, int Q, int RW>
 __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_attn_kernel(
     const AttnArgs a) {
-  constexpr int D = 32 * NB, WT = 4 / RW, WROWS = 4 * Q, ROWS = WROWS * RW, NW = (NB + 1) / 2;
+  constexpr int WAVES = kAttnThreads / 64, D = 32 * NB, WT = WAVES / RW, WROWS = 4 * Q, ROWS = WROWS * RW, NW = (NB + 1) / 2;
   constexpr int C = NB / 2;                 // whole chunks of 64 values
   constexpr bool HALF = NB % 2 != 0;        // and a chunk of 32
   constexpr int CA = C + (HALF ? 1 : 0);
   constexpr int ES = I8 ? 1 : 2;
+  // Wide heads of halves: no registers for a second tile's values, the next tile's are
+  // requested when this one's have been used.
+  constexpr bool LATE = !I8 && NB >= 7;
   using Reg = std::conditional_t<I8, uint2, uint4>;   // eight codes or halves
   __shared__ uint32_t cum[kMaxAttnSeqs + 1];
   __shared__ int32_t len_of[kMaxAttnSeqs];
-  __shared__ uint32_t wave_sum[4];
-  __shared__ float2 wave_ml[4][WROWS];
-  __shared__ float sums[4][WROWS][D + 4];
-  __shared__ float weights[4][WROWS][36];
+  __shared__ uint32_t wave_sum[WAVES];
+  __shared__ float2 wave_ml[WAVES][WROWS];
+  __shared__ float weights[WAVES][WROWS][40];
+  // The queries, two halves each as the first product takes them; once the tiles are
+  // done, the waves' sums.
+  __shared__ union Shared {
+    half8v queries[RW][NB][2][64];
+    float sums[WAVES][WROWS][D + 4];
+    __device__ Shared() {}
+  } sh;
 
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wr = wave % RW, wt = wave / RW;
   const int64_t cap = (int64_t)a.c.max_pages << a.c.page_shift;
 
-  // ---- the line of tiles: cum[b] = tiles of one item of sequences before b
+  // ---- the line of tiles: cum[b] = length of one item of the sequences before b, its
+  // tiles and what starting on it costs (one sequence is cut by tiles alone)
+  const uint32_t start = a.B == 1 ? 0 : kAttnItemStart;
   {
     const int tid = threadIdx.x, lane = tid & 63;
-    uint32_t nt[4], mine = 0;
+    constexpr int EACH = kMaxAttnSeqs / kAttnThreads;   // sequences of a thread
+    uint32_t nt[EACH], mine = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = 4 * tid + i;
+    for (int i = 0; i < EACH; ++i) {
+      const int b = EACH * tid + i;
       nt[i] = 0;
       if (b < a.B) {
         const int32_t len = a.lens[b];
@@ -162,13 +174,13 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
           if (a.err && blockIdx.x == 0) *a.err = 1;
         } else if (len > 0) {
           const int64_t lo = a.window > 0 ? max((int64_t)0, len - a.T - a.window + 1) : 0;
-          nt[i] = (uint32_t)((((int64_t)len + 31) >> 5) - (lo >> 5));
+          nt[i] = (uint32_t)((((int64_t)len + 31) >> 5) - (lo >> 5)) + start;
         }
       }
       mine += nt[i];
     }
     uint32_t inc = mine;
-    if (a.B > 4) {
+    if (a.B > EACH) {
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
         const uint32_t o = __shfl_up(inc, off, 64);
@@ -176,16 +188,16 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
       }
     }
     uint32_t at = inc - mine;
-    if (a.B > 256) {
+    if (a.B > 64 * EACH) {
       if (lane == 63) wave_sum[wave] = inc;
       __syncthreads();
       for (int w = 0; w < wave; ++w) at += wave_sum[w];
     }
     if (tid == 0) cum[0] = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < EACH; ++i) {
       at += nt[i];
-      if (4 * tid + i < a.B) cum[4 * tid + i + 1] = at;
+      if (EACH * tid + i < a.B) cum[EACH * tid + i + 1] = at;
     }
     __syncthreads();
   }
@@ -225,15 +237,16 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
 
   for (int64_t unit = first_unit; unit < end_unit;) {
     while (unit >= (int64_t)line(b + 1) * items) ++b;       // sequences without tiles
-    int64_t nt = line(b + 1) - cum[b];
+    const int64_t length = line(b + 1) - cum[b];
     const int64_t in_seq = unit - (int64_t)cum[b] * items;
-    const int item = (int)divided(in_seq, nt);
-    const int t0 = (int)(in_seq - item * nt);
-    const int slot = unit == first_unit ? 0 : 1;
-    const int64_t here_ = min(nt - t0, end_unit - unit);
-    unit += here_;
-    if (alike) nt = cum[1];                                  // without the rounding up
-    const int t1 = (int)min(nt, t0 + here_);
+    const int item = (int)divided(in_seq, length);
+    const int64_t from = in_seq - item * length;             // of the item
+    const int64_t to = min(length, from + (end_unit - unit));
+    const int slot = unit == first_unit && from >= start ? 0 : 1;
+    unit += to - from;
+    const int nt = (int)((alike ? cum[1] : length) - start);
+    const int t0 = (int)max((int64_t)0, from - start), t1 = (int)min((int64_t)nt, to - start);
+    if (t0 >= t1) continue;                                  // the share ends before the tiles
     const bool whole = t0 == 0 && t1 == nt;
 
     const int kvh = item / a.row_groups, rg = item - kvh * a.row_groups;
@@ -312,13 +325,12 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
       }
     };
 
-    int t = t0 + wt;
+    int t = wr * WROWS < rows_all - rg * ROWS ? t0 + wt : t1;     // (a wave may have no rows)
     int32_t pk = 0, pv = 0;                 // pages of the next tile's keys and values
+    const int last = t < t1 ? t + (t1 - 1 - t) / WT * WT : t;     // this wave's last tile
     auto next_pages = [&](int u) {
-      if (u < t1) {
-        pk = page_of(4 * (tile0 + u) + gk);
-        pv = page_of(4 * (tile0 + u) + g);
-      }
+      pk = page_of(4 * (tile0 + min(u, last)) + gk);
+      pv = page_of(4 * (tile0 + min(u, last)) + g);
     };
     next_pages(t);
 
@@ -343,11 +355,11 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
       }
     }
     if (t < t1) {
-      load_k(tile0 + t, pk, pv);
-      load_v(va, tile0 + t, pv);
+      const int32_t pk1 = pk, pv1 = pv;
       next_pages(t + WT);
+      load_k(tile0 + t, pk1, pv1);
+      load_v(va, tile0 + t, pv1);
     }
-    half8v qh[NB], ql[NB];
     float c;                                                // score -> base 2, unscaled
     {
       float big = 0.0f;
@@ -364,10 +376,17 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
       for (int k = 0; k < NB; ++k) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) qx[k][i] *= up;
-        split8(qx[k], qh[k], ql[k]);
+        half8v hi, lo_;
+        split8(qx[k], hi, lo_);
+        if (wt == 0) {                      // (the waves of one row tile hold the same)
+          sh.queries[wr][k][0][lane_q] = hi;
+          sh.queries[wr][k][1][lane_q] = lo_;
+        }
       }
       c = a.scale * 1.44269504088896340736f * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
     }
+
+    __syncthreads();
 
     // ---- the stream of tiles
     float4v o[CA][Q];                       // lane: value 64 i + lane of four query rows
@@ -385,7 +404,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
         constexpr int u = uc;
         float w[Q], s[CA];
 #pragma unroll
-        for (int q = 0; q < Q; ++q) w[q] = w0[(4 * q) * 36 + 8 * u];
+        for (int q = 0; q < Q; ++q) w[q] = w0[(4 * q) * 40 + 8 * u];
 #pragma unroll
         for (int k = 0; k < C; ++k)
           s[k] = scaled_by_s ? lane_of(v.s[k], 16 * u + 8 * (lane >> 5) + ((lane >> 2) & 7)) : 1.0f;
@@ -409,7 +428,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
                           : 1.0f;
           float w[Q];
 #pragma unroll
-          for (int q = 0; q < Q; ++q) w[q] = wh[(4 * q) * 36 + 8 * u] * s;
+          for (int q = 0; q < Q; ++q) w[q] = wh[(4 * q) * 40 + 8 * u] * s;
           unrolled<0, 8>([&](auto jc) {
             constexpr int j = jc;
             const float x = of(value_of<j>(v.h[u]));
@@ -432,50 +451,45 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
     // One tile: its values lie in `v`, the next tile's go to `next`.
     auto step = [&](Values& v, Values& next) {
       const int tile = tile0 + t;
-      const bool more = t + WT < t1;
       // scores: x[4 s + i] of token 8 g + 4 s + i
       float x[8];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        float4v acc = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (I8) {
-          unrolled<0, NB>([&](auto kc) {
-            constexpr int k = kc;
+      {
+        const half8v* qp = &sh.queries[wr][0][0][lane];
+        const float4v zero = {0.f, 0.f, 0.f, 0.f};
+        float4v acc[2] = {zero, zero}, low[2] = {zero, zero};
+        unrolled<0, NB>([&](auto kc) {
+          constexpr int k = kc;
+          const half8v hi = qp[(2 * k) * 64], lo_ = qp[(2 * k + 1) * 64];
+          unrolled<0, 2>([&](auto sc) {
+            constexpr int s = sc;
             const half8v kk = halves_of(key.r[s][k]);
-            float4v part = {0.f, 0.f, 0.f, 0.f};
-            part = mfma(kk, qh[k], part);
-            part = mfma(kk, ql[k], part);
-            if (s == 0) {
+            if constexpr (I8) {
+              const float4v part = mfma(kk, lo_, mfma(kk, hi, zero));
               unrolled<0, 4>([&](auto ic) {
                 constexpr int i = ic;
-                acc[i] += scaled(row_bcast<(k & 1) * 8 + i>(key.s[k >> 1]), part[i]);
+                acc[s][i] += scaled(row_bcast<(k & 1) * 8 + 4 * s + i>(key.s[k >> 1]), part[i]);
               });
             } else {
-              unrolled<0, 4>([&](auto ic) {
-                constexpr int i = ic;
-                acc[i] += scaled(row_bcast<(k & 1) * 8 + 4 + i>(key.s[k >> 1]), part[i]);
-              });
+              acc[s] = mfma(kk, hi, acc[s]);
+              low[s] = mfma(kk, lo_, low[s]);
             }
           });
-        } else {
+        });
 #pragma unroll
-          for (int k = 0; k < NB; ++k) {
-            acc = mfma(halves_of(key.r[s][k]), qh[k], acc);
-            acc = mfma(halves_of(key.r[s][k]), ql[k], acc);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[4 * s + i] = acc[i] * c;
-          asm volatile("" : "+v"(x[4 * s + i]));   // not put off until after the loads
+        for (int j = 0; j < 8; ++j) {
+          x[j] = (acc[j >> 2][j & 3] + low[j >> 2][j & 3]) * c;
+          asm volatile("" : "+v"(x[j]));    // not put off until after the loads
         }
       }
-      // the next tile's keys and values are on their way while this one is worked on
-      if (more) {
-        load_k(tile + WT, pk, pv);
-        load_v(next, tile + WT, pv);
-        next_pages(t + 2 * WT);
-      }
+      // The next tile's keys and values are on their way while this one is worked on.  The
+      // pages after them are requested first: loads return in order.  The last tile
+      // requests itself again (out of the cache), because requests that only some
+      // iterations make would have to be waited for as if none had been made since.
+      const int32_t pk1 = pk, pv1 = pv;
+      const int ahead = tile0 + min(t + WT, last);
+      next_pages(t + 2 * WT);
+      load_k(ahead, pk1, pv1);
+      if constexpr (!LATE) load_v(next, ahead, pv1);
 
       // visibility: only a tile at an end of the sequence or of a window has hidden tokens
       const int pos0 = 32 * tile + 8 * g;
@@ -608,11 +622,16 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
       }
       put_weights(p);
       add_products(v, o, std::bool_constant<I8>{}, [](float f) { return f; });
+      if constexpr (LATE) load_v(next, ahead, pv1);
       t += WT;
     };
     while (t < t1) {
-      step(va, vb);
-      if (t < t1) step(vb, va);
+      if constexpr (LATE) {
+        step(va, va);
+      } else {
+        step(va, vb);
+        if (t < t1) step(vb, va);
+      }
     }
 
     // ---- the waves' sums together, then out: finished, or into this share's slot
@@ -630,11 +649,11 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
       constexpr int r = rc;
       const float f = row_bcast<r>(fix);
 #pragma unroll
-      for (int k = 0; k < C; ++k) sums[wave][r][64 * k + lane_] = o[k][r >> 2][r & 3] * f;
+      for (int k = 0; k < C; ++k) sh.sums[wave][r][64 * k + lane_] = o[k][r >> 2][r & 3] * f;
       if constexpr (HALF) {
         const float h = o[C][r >> 2][r & 3] * f;
         const float both = h + __shfl_xor(h, 32, 64);
-        if (lane_ < 32) sums[wave][r][64 * C + lane_] = both;
+        if (lane_ < 32) sh.sums[wave][r][64 * C + lane_] = both;
       }
     });
     __syncthreads();
@@ -650,7 +669,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
       for (int w = 0; w < WT; ++w) {
         const float2 ml = wave_ml[w * RW + tile_r][rn];
         ll += ml.y * __builtin_amdgcn_exp2f(ml.x - mm);
-        const float4 u = *reinterpret_cast<const float4*>(&sums[w * RW + tile_r][rn][d]);
+        const float4 u = *reinterpret_cast<const float4*>(&sh.sums[w * RW + tile_r][rn][d]);
         s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w;
       }
       const int gr = rg * ROWS + r, gt = gr / a.group;
@@ -676,6 +695,7 @@ hipError_t launch_attn(const AttnArgs& a, int rows, int grid, hipStream_t stream
                       : rows <= 8  ? paged_attn_kernel<I8, NB, 2, 1>
                       : rows <= 16 ? paged_attn_kernel<I8, NB, 4, 1>
                       : rows <= 32 ? paged_attn_kernel<I8, NB, 4, 2>
+                      : rows <= 48 ? paged_attn_kernel<I8, NB, 3, 4>
                                    : paged_attn_kernel<I8, NB, 4, 4>;
   hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(kAttnThreads), 0, stream, a);
   return hipGetLastError();
