@@ -64,6 +64,19 @@ constexpr int attn_waves(bool i8, int nb, int q) {
   return nb <= 4 ? (q == 1 ? 3 : 2) : (nb <= 6 && q <= 2) || q == 1 ? 2 : 1;
 }
 
+// a / b for a >= 0, b > 0: by way of a reciprocal while the numbers are small (the full
+// division is a long chain of instructions that every workgroup waits for).
+__device__ __forceinline__ int64_t divided(int64_t a, int64_t b) {
+  if ((a | b) < (int64_t(1) << 22)) {
+    const int x = (int)a, y = (int)b;
+    int q = (int)((float)x * __builtin_amdgcn_rcpf((float)y));    // off by one at most
+    const int rest = x - q * y;
+    q += rest >= y ? 1 : rest < 0 ? -1 : 0;
+    return q;
+  }
+  return a / b;
+}
+
 struct AttnArgs {
   KvView c;
   const float* q;
@@ -71,7 +84,7 @@ struct AttnArgs {
   float* y;
   int32_t* err;
   int64_t q_stride;
-  int64_t window;
+  int32_t window;                         // 0: none
   float scale;
   int32_t B, T, H;
   int32_t group;                          // query heads to a key/value head

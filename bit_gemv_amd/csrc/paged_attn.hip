@@ -11,6 +11,9 @@ int item_rows(int64_t rows) {
   return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
 }
 
+// Rows up to which the join gives each a workgroup for every 32 values.
+constexpr int64_t kWideJoinRows = 256;
+
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
@@ -27,81 +30,112 @@ Layout layout(int64_t dim, int64_t B, int64_t rows) {
   return l;
 }
 
-// One workgroup per query row: the parts of its item, if there are several, are
-// summed with the weights exp2(m_i - m).  D / 4 lanes side by side take the
-// row's values, the rest of the workgroup other parts.  Also writes the rows
-// that no tile belongs to: sequences without tokens (zeros) or with an
-// impossible length (NaN).
+// Joins the parts of an item that several workgroups worked on: their sums, with the
+// weights exp2(m_i - m).  Also writes the rows that no tile belongs to: sequences without
+// tokens (zeros) or with an impossible length (NaN).
+//
+// WIDE: a workgroup for 32 values of one row (a few rows in many parts: one long
+// sequence), eight lanes side by side, 32 parts at once.  Otherwise a wave for each row
+// (many rows, most of them in one or two parts or none at all to join).
+template <bool WIDE>
 __global__ __launch_bounds__(kJoinThreads) void paged_attn_join_kernel(const AttnArgs a,
                                                                        int rows_of_item) {
+  constexpr int TEAM = WIDE ? kJoinThreads : 64;    // threads of a row (or of 32 values of it)
   __shared__ float red[kJoinThreads / 64];
-  __shared__ float4 acc[kJoinThreads];
-  __shared__ float accl[kJoinThreads];
-  const int D = a.c.dim, tid = threadIdx.x;
-  const int64_t row = blockIdx.x;                   // (b * T + t) * H + h
-  const int h = (int)(row % a.H);
-  const int64_t bt = row / a.H;
-  const int t = (int)(bt % a.T), b = (int)(bt / a.T);
+  __shared__ float4 acc[WIDE ? 4 : 1][8];
+  __shared__ float accl[4];
+  const int D = a.c.dim, tid = threadIdx.x % TEAM;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int chunks = WIDE ? D >> 5 : 1;
+  const uint32_t task = WIDE ? blockIdx.x / chunks : blockIdx.x * 4 + wave;
+  const int row = (int)task;                        // (b * T + t) * H + h
+  if (row >= a.B * a.T * a.H) return;
+  const int bt = row / a.H, h = row - bt * a.H;
+  const int b = bt / a.T, t = bt - b * a.T;
+  const int quads = WIDE ? 8 : D >> 2;              // lanes that hold a part's values
+  const int quad0 = WIDE ? 8 * (int)(blockIdx.x - task * chunks) : 0;
+  const int lane = tid % quads, group = tid / quads, groups = TEAM / quads;
+  float4* out = reinterpret_cast<float4*>(a.y + (int64_t)row * D) + quad0;
   const int64_t length = a.cum[b + 1] - a.cum[b];   // of an item of this sequence
+  const int64_t share = a.plan[0];
+  const int len = a.lens[b];
   const int start = a.B == 1 ? 0 : kAttnItemStart;
-  const int lanes = D >> 2;                         // 8 .. 64
-  const int lane = tid % lanes, group = tid / lanes, groups = kJoinThreads / lanes;
-  const bool active = group < groups;
-  float4* out = reinterpret_cast<float4*>(a.y + row * D);
   if (length == 0) {
-    const float v = a.lens[b] > 0 ? __builtin_nanf("") : 0.0f;
-    if (tid < lanes) out[tid] = make_float4(v, v, v, v);
+    const float v = len > 0 ? __builtin_nanf("") : 0.0f;
+    if (tid < quads) out[tid] = make_float4(v, v, v, v);
     return;
   }
   const int kvh = h / a.group;
   const int r = t * a.group + (h - kvh * a.group);
   const int rg = r / rows_of_item;
-  const int64_t share = a.plan[0];
   const int64_t items = (int64_t)a.c.heads * a.row_groups;
   const int64_t first =
       (int64_t)a.cum[b] * items + (int64_t)(kvh * a.row_groups + rg) * length + start;
-  const int64_t w0 = first / share, w1 = (first + length - start - 1) / share;
+  const int64_t w0 = divided(first, share), w1 = divided(first + length - start - 1, share);
   if (w0 == w1) return;                             // written by its one workgroup
   const int parts = (int)(w1 - w0 + 1);
   // part i is slot 0 of workgroup w0 + i, but for a first one that starts inside its share
-  const int64_t r_in = r - rg * rows_of_item;
-  auto at = [&](int i) {
-    const int64_t w = w0 + i;
-    const int slot = i == 0 && first != w0 * share ? 1 : 0;
-    return (2 * w + slot) * a.slot_rows + r_in;
-  };
+  const int64_t at0 = (2 * w0 + (first != w0 * share ? 1 : 0)) * a.slot_rows + (r - rg * rows_of_item);
+  const int64_t at1 = 2 * w0 * a.slot_rows + (r - rg * rows_of_item);
+  auto at = [&](int i) { return i == 0 ? at0 : at1 + (int64_t)(2 * i) * a.slot_rows; };
   float m = -INFINITY;
-  for (int i = tid; i < parts; i += kJoinThreads) m = fmaxf(m, a.ml[at(i)].x);
+  for (int i = tid; i < parts; i += TEAM) m = fmaxf(m, a.ml[at(i)].x);
+#pragma unroll
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  if ((tid & 63) == 0) red[tid >> 6] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  if constexpr (WIDE) {
+    if ((tid & 63) == 0) red[wave] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  }
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.0f;
-  if (active) {
+  if (group < groups) {
 #pragma unroll 4
     for (int i = group; i < parts; i += groups) {
       const int64_t k = at(i);
       const float2 ml = a.ml[k];
-      const float4 p = reinterpret_cast<const float4*>(a.part + k * D)[lane];
+      const float4 p = reinterpret_cast<const float4*>(a.part + k * D)[quad0 + lane];
       const float f = __builtin_amdgcn_exp2f(ml.x - m);
       l += f * ml.y;
       s.x += f * p.x; s.y += f * p.y; s.z += f * p.z; s.w += f * p.w;
     }
   }
-  acc[tid] = s;
-  accl[tid] = l;
-  __syncthreads();
-  if (tid < lanes) {
-    for (int i = 1; i < groups; ++i) {
-      const float4 p = acc[i * lanes + tid];
-      s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
-      l += accl[i * lanes + tid];
+  // the groups of a wave together: group g's lanes are g * quads further on
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int off = 8; off < 64; off <<= 1) {
+      s.x += __shfl_xor(s.x, off, 64); s.y += __shfl_xor(s.y, off, 64);
+      s.z += __shfl_xor(s.z, off, 64); s.w += __shfl_xor(s.w, off, 64);
+      l += __shfl_xor(l, off, 64);
     }
+    if ((tid & 63) < 8) acc[wave][tid & 7] = s;
+    if ((tid & 63) == 0) accl[wave] = l;
+    __syncthreads();
+    if (tid < 8) {
+      s = make_float4(0.f, 0.f, 0.f, 0.f);
+      l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float4 p = acc[w][tid];
+        s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
+        l += accl[w];
+      }
+    }
+  } else {
+    const float4 s0 = s;
+    const float l0 = l;
+    for (int g = 1; g < groups; ++g) {
+      const int from = (tid + g * quads) & 63;
+      s.x += __shfl(s0.x, from, 64); s.y += __shfl(s0.y, from, 64);
+      s.z += __shfl(s0.z, from, 64); s.w += __shfl(s0.w, from, 64);
+      l += __shfl(l0, from, 64);
+    }
+  }
+  if (tid < quads) {
     const float f = 1.0f / l;
-    const bool none = a.lens[b] - a.T + t < 0;      // a row that sees nothing
-    out[tid] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                    : make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
+    const bool none = len - a.T + t < 0;            // a row that sees nothing
+    out[lane] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                     : make_float4(s.x * f, s.y * f, s.z * f, s.w * f);
   }
 }
 
@@ -127,7 +161,8 @@ hipError_t launch_paged_attn(const KvView& c, bool i8, const float* q, int64_t B
   a.y = y;
   a.err = err;
   a.q_stride = q_stride;
-  a.window = window;
+  // positions are below 2^31, so a window of that size hides nothing
+  a.window = window < (int64_t(1) << 31) - 16 ? (int32_t)window : 0;
   a.scale = scale;
   a.B = (int)B;
   a.T = (int)new_tokens;
@@ -152,8 +187,13 @@ hipError_t launch_paged_attn(const KvView& c, bool i8, const float* q, int64_t B
                                 : launch_paged_attn_78;
   hipError_t e = launch(a, i8, nb, (int)std::min<int64_t>(rows, 64), grid, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(paged_attn_join_kernel, dim3((uint32_t)(B * new_tokens * H)),
-                     dim3(kJoinThreads), 0, stream, a, ir);
+  const int64_t out_rows = B * new_tokens * H;
+  if (out_rows <= kWideJoinRows)
+    hipLaunchKernelGGL(paged_attn_join_kernel<true>, dim3((uint32_t)(out_rows * nb)),
+                       dim3(kJoinThreads), 0, stream, a, ir);
+  else
+    hipLaunchKernelGGL(paged_attn_join_kernel<false>, dim3((uint32_t)((out_rows + 3) / 4)),
+                       dim3(kJoinThreads), 0, stream, a, ir);
   return hipGetLastError();
 }
 

@@ -32,6 +32,13 @@ __device__ __forceinline__ float scaled(float scale, float x) {
   return y;
 }
 
+// The number of the lane that a shift or broadcast (CTRL) names, in the given rows of 16
+// lanes; 0 in the others and where there is no such lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t from_lane(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
+}
+
 __device__ __forceinline__ float max_over_groups(float x) {     // lanes l, l^16, l^32, l^48
   x = fmaxf(x, __shfl_xor(x, 16, 64));
   return fmaxf(x, __shfl_xor(x, 32, 64));
@@ -103,11 +110,6 @@ __device__ __forceinline__ float lane_of(float x, int lane) {
   return __int_as_float(__builtin_amdgcn_ds_bpermute(4 * lane, __float_as_int(x)));
 }
 
-// a / b where both mostly fit 32 bits
-__device__ __forceinline__ int64_t divided(int64_t a, int64_t b) {
-  return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
 // LDS written by some lanes of a wave, read by others of it: the accesses execute in
 // order, the compiler has to keep them so.
 __device__ __forceinline__ void wave_fence() {
@@ -173,19 +175,21 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
         if (len > cap) {
           if (a.err && blockIdx.x == 0) *a.err = 1;
         } else if (len > 0) {
-          const int64_t lo = a.window > 0 ? max((int64_t)0, len - a.T - a.window + 1) : 0;
-          nt[i] = (uint32_t)((((int64_t)len + 31) >> 5) - (lo >> 5)) + start;
+          const int lo = a.window > 0 ? max(0, len - a.T - a.window + 1) : 0;
+          nt[i] = (uint32_t)(((len - 1) >> 5) + 1 - (lo >> 5)) + start;
         }
       }
       mine += nt[i];
     }
+    // sum over the lanes up to this one, inside rows of 16, then over the rows
     uint32_t inc = mine;
     if (a.B > EACH) {
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const uint32_t o = __shfl_up(inc, off, 64);
-        if (lane >= off) inc += o;
-      }
+      inc += from_lane<0x111, 0xF>(inc);
+      inc += from_lane<0x112, 0xF>(inc);
+      inc += from_lane<0x114, 0xF>(inc);
+      inc += from_lane<0x118, 0xF>(inc);
+      inc += from_lane<0x142, 0xA>(inc);
+      inc += from_lane<0x143, 0xC>(inc);
     }
     uint32_t at = inc - mine;
     if (a.B > 64 * EACH) {
@@ -252,7 +256,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
     const int kvh = item / a.row_groups, rg = item - kvh * a.row_groups;
     const int rows_all = a.T * a.group;
     const int len = __builtin_amdgcn_readfirstlane(len_of[b]);
-    const int lo = a.window > 0 ? (int)max((int64_t)0, len - a.T - a.window + 1) : 0;
+    const int lo = a.window > 0 ? max(0, len - a.T - a.window + 1) : 0;
     const int tile0 = lo >> 5;
     const int group_lo = lo >> 3, group_hi = (len - 1) >> 3;
 
@@ -501,7 +505,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
         if (a.err) *a.err = 1;
       }
       if (edge) {
-        const int from = a.window > 0 ? (int)max((int64_t)-1, row_pos - a.window) + 1 : 0;
+        const int from = a.window > 0 ? row_pos - a.window + 1 : 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (pos0 + j > row_pos || pos0 + j < from) x[j] = -INFINITY;
