@@ -174,8 +174,8 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(
     load4(x, src + d);
     if (!is_v && r.rot) turn4(x, src, d, r, table[tt]);
     if (is_q) {
-      *reinterpret_cast<float4*>(q_out + t * q_out_stride + (int64_t)h * D + d) =
-          make_float4(x[0], x[1], x[2], x[3]);
+      store4<(TG > 1)>(q_out + t * q_out_stride + (int64_t)h * D + d,
+                       make_float4(x[0], x[1], x[2], x[3]));
       continue;
     }
     const int32_t page = s.page[tt], row = s.row[tt];
@@ -314,7 +314,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(
       }
     }
     float* dst = is_v ? v + t * v_stride : k + t * k_stride;
-    *reinterpret_cast<float4*>(dst + (int64_t)h * D + d) = x;
+    store4<(TG > 1)>(dst + (int64_t)h * D + d, x);
   }
   if constexpr (TG > 1) {
     if (together) {
@@ -347,8 +347,8 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(
         }
 #pragma unroll
         for (int i = 0; i < TG; ++i)
-          *reinterpret_cast<float4*>(v + (t0 + i) * v_stride + (int64_t)h * D + d) =
-              make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+          store4<true>(v + (t0 + i) * v_stride + (int64_t)h * D + d,
+                       make_float4(x[i][0], x[i][1], x[i][2], x[i][3]));
       }
     }
   }
@@ -364,10 +364,11 @@ hipError_t launch_kv_write(const KvView& c, bool i8, const float* q, const float
   const bool wide = T >= kGroupTokens;
   const int heads = (int)H + 2 * c.heads;
   const int64_t blocks = wide ? T / 8 + 2 : T;
-  // One pass of a workgroup's threads over the heads where few tokens would leave
-  // compute units idle, all heads (the angles are computed once) where not.
-  const int slots = kThreads / (c.dim / 4);
-  const int per = blocks >= 512 ? heads : slots;
+  // A workgroup takes one pass of its threads over the heads (eight heads of 128
+  // values), and computes the angles of its tokens for itself: at 4001 tokens of 32 heads
+  // the write and read-back take 41 us, 54 us with half the heads a workgroup and 64 us
+  // with all of them (502 workgroups, each a long chain).
+  const int per = kThreads / (c.dim / 4);
   const auto kernel = wide ? (i8 ? kv_write_kernel<true, 8> : kv_write_kernel<false, 8>)
                            : (i8 ? kv_write_kernel<true, 1> : kv_write_kernel<false, 1>);
   hipLaunchKernelGGL(kernel, dim3((uint32_t)blocks, (uint32_t)((heads + per - 1) / per)),

@@ -7,6 +7,17 @@
 
 namespace rfp2 {
 
+// Sixteen bytes to memory that nobody reads soon: past the caches (NT), which a large
+// output would only sweep.  Read-back of 20011 tokens of 8 heads of 128: 53.2 us with
+// ordinary stores, 34.6 us so.
+template <bool NT>
+__device__ __forceinline__ void store4(float* p, float4 x) {
+  typedef float vec4 __attribute__((ext_vector_type(4)));
+  const vec4 v = {x.x, x.y, x.z, x.w};
+  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<vec4*>(p));
+  else *reinterpret_cast<vec4*>(p) = v;
+}
+
 // The page of token pos of sequence seq, or -1 where the cache has no such
 // token (or the table names no page of it).
 __device__ __forceinline__ int32_t kv_page(const KvView& c, int32_t seq, int32_t pos) {

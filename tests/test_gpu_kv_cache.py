@@ -69,6 +69,9 @@ def tokens(T, H, D, seed):
 CASES = [  # T, H, D, P, first position, sequences
     (1, 1, 32, 8, 0, 1), (1, 8, 128, 64, 4095, 1), (5, 2, 96, 16, 3, 5), (48, 8, 128, 64, 11, 48),
     (77, 3, 64, 8, 5, 1), (77, 1, 256, 32, 30, 1), (200, 2, 160, 128, 0, 2), (129, 4, 224, 16, 7, 3),
+    # eight tokens a workgroup: starting inside a group of the cache, ending inside one, and
+    # tokens that do not lie together
+    (515, 2, 64, 16, 5, 1), (1024, 1, 256, 64, 0, 1), (700, 3, 96, 8, 3, 3), (513, 1, 32, 128, 127, 1),
 ]
 
 
@@ -105,21 +108,23 @@ def test_write_and_read_back(fmt, T, H, D, P, first, seqs):
 
 
 @pytest.mark.parametrize("fmt", [rf.KV_F16, rf.KV_I8])
+@pytest.mark.parametrize("T", [37, 557])
 @pytest.mark.parametrize("rot,inter", [(64, False), (64, True), (38, False), (38, True), (2, True), (62, False)])
-def test_fused_equals_the_separate_calls(fmt, rot, inter):
-    announce("rope_kv_write", fmt, rot, inter)
-    T, Hq, H, D, P = 37, 6, 2, 64, 16
+def test_fused_equals_the_separate_calls(fmt, rot, inter, T):
+    announce("rope_kv_write", fmt, rot, inter, T)
+    Hq, H, D, P = 6, 2, 64, 16
+    pages = -(-(T + 5) // P) + 4
     rng = np.random.default_rng(rot)
     qkv = to_dev(rng.standard_normal((T, (Hq + 2 * H) * D)).astype(np.float32))
     q, k, v = qkv.split([Hq * D, H * D, H * D], 1)
-    table = rng.permutation(8)[:4].reshape(1, 4)
+    table = rng.permutation(pages)[:pages - 4].reshape(1, -1)
     seq, pos = np.zeros(T, np.int32), (5 + np.arange(T)).astype(np.int32)
     seq[3] = 1                      # outside the cache: not stored, q rotated all the same
     pos[4] = -2                     # padding
     sg, pg = to_dev(seq), to_dev(pos)
     f = to_dev(oa.rope_freqs(rot, 10000.0))
     style = rf.ROPE_INTERLEAVED if inter else rf.ROPE_HALF
-    a, b, e = (make_cache(fmt, 8, P, H, D, table) for _ in range(3))
+    a, b, e = (make_cache(fmt, pages, P, H, D, table) for _ in range(3))
     e1, e2 = (torch.zeros(1, dtype=torch.int32, device=device()) for _ in range(2))
     q1, q2, k2 = empty((T, Hq * D), torch.float32), empty((T, Hq, D), torch.float32), empty((T, H * D), torch.float32)
     rf.rfp2_rope_kv_write(a, q, k, v, T, Hq, sg, pg, f, rot, style, 1.1, q1, e1)
@@ -133,7 +138,7 @@ def test_fused_equals_the_separate_calls(fmt, rot, inter):
         if x is not None:
             assert same_bits(host(x), host(y)) and same_bits(host(x), host(z))
     assert int(host(e1)[0]) == int(host(e2)[0]) == 1
-    ref = expected(fmt, 8, P, H, D, table, host(k2).reshape(T, H, D),
+    ref = expected(fmt, pages, P, H, D, table, host(k2).reshape(T, H, D),
                    host(v.contiguous()).reshape(T, H, D), seq, pos)
     assert_cache(a, ref)
 

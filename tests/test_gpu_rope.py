@@ -40,6 +40,7 @@ CASES = [  # T, H, D, rot, interleaved, first position, factor
     (33, 8, 64, 64, True, 5, 1.0), (5, 2, 96, 22, False, 131071, 1.0), (5, 2, 96, 22, True, 131071, 4.0),
     (3, 17, 256, 256, False, 1 << 20, 1.0), (2, 1, 1024, 1024, True, 1 << 20, 1.0),
     (2, 5, 20, 6, False, -9, 1.0), (300, 6, 128, 120, False, 0, 1.0), (1, 64, 192, 190, True, 12, 1.0),
+    (600, 3, 128, 128, False, 9, 1.0), (530, 5, 64, 32, True, 70000, 4.0), (512, 2, 96, 30, False, 3, 1.0),
 ]
 
 
