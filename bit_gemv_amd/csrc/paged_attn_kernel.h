@@ -106,6 +106,24 @@ __device__ __forceinline__ float value_of(uint4 w) {
   return (float)halves_of(w)[J];
 }
 
+// Values that one wave alone reads go past the caches (ONCE): 317 -> 306 us at 128 sequences
+// of up to 8000 tokens; keys, whose lines two or more loads share, must not (388 us).
+template <bool ONCE, class R>
+__device__ __forceinline__ R load_values(const R* p) {
+  typedef uint32_t vec __attribute__((ext_vector_type(sizeof(R) / 4)));
+  if constexpr (!ONCE) return *p;
+  union { vec v; R r; } o;
+  o.v = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p));
+  return o.r;
+}
+
+// Lanes 32..63 of a for lanes 0..31 of b.
+__device__ __forceinline__ void trade_halves(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
 __device__ __forceinline__ float lane_of(float x, int lane) {
   return __int_as_float(__builtin_amdgcn_ds_bpermute(4 * lane, __float_as_int(x)));
 }
@@ -264,7 +282,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
 
     // ---- the cache's tiles
     struct Keys {                           // a tile's keys and their scales
-      Reg r[2][NB];
+      uint4 w[2][I8 ? C + 1 : NB];          // int8: 64 values a load, the half chunk's last
       float s[NW];
     } key;
     struct Values {                         // a tile's values, their scales, no such page
@@ -286,14 +304,23 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
              ((grp << 3) & ((1 << a.c.page_shift) - 1));
     };
     const int gk = n >> 2;                  // token group of this lane's key rows
+    // the first of a lane's eight values in a block of 32
+    auto dim_of = [](int g) { return I8 ? 16 * (g & 1) + 8 * (g >> 1) : 8 * g; };
     auto load_k = [&](int tile, int32_t page, int32_t page_s) {
       const int64_t r = rows_of(4 * tile + gk, page) + (n & 3);
-      const char* p = static_cast<const char*>(a.c.k) + (r * D + 8 * g) * ES;
+      const char* p = static_cast<const char*>(a.c.k) + r * D * ES + 16 * g;
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < 2; ++s) {
 #pragma unroll
-        for (int k = 0; k < NB; ++k)
-          key.r[s][k] = *reinterpret_cast<const Reg*>(p + (4 * s * D + 32 * k) * ES);
+        for (int k = 0; k < (I8 ? C : NB); ++k)
+          key.w[s][k] = *reinterpret_cast<const uint4*>(p + 4 * s * D * ES + 64 * k);
+        if constexpr (I8 && HALF) {
+          const uint2 h = *reinterpret_cast<const uint2*>(
+              p - 16 * g + dim_of(g) + 4 * s * D + 64 * C);
+          key.w[s][C].x = h.x;
+          key.w[s][C].y = h.y;
+        }
+      }
       if constexpr (I8) {
         const int64_t rs = rows_of(4 * tile + g, page_s);
 #pragma unroll
@@ -312,7 +339,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
         const char* p = static_cast<const char*>(a.c.v) + r[u] * D * ES;
 #pragma unroll
         for (int k = 0; k < C; ++k)
-          v.r[u][k] = *reinterpret_cast<const Reg*>(p + (lane + 64 * k) * 8 * ES);
+          v.r[u][k] = load_values<RW == 1>(reinterpret_cast<const Reg*>(p + (lane + 64 * k) * 8 * ES));
       }
       if constexpr (HALF) {                 // lanes 32 .. 63: the same values, two groups on
 #pragma unroll
@@ -347,7 +374,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
     const int row_pos = len - a.T + row_t;                  // this row's position
     float qx[NB][8];
     {
-      const float* qp = a.q + ((int64_t)b * a.T + row_t) * a.q_stride + (int64_t)row_h * D + 8 * gq;
+      const float* qp = a.q + ((int64_t)b * a.T + row_t) * a.q_stride + (int64_t)row_h * D + dim_of(gq);
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         const float4 u = row_ok ? *reinterpret_cast<const float4*>(qp + 32 * k)
@@ -466,14 +493,22 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
           const half8v hi = qp[(2 * k) * 64], lo_ = qp[(2 * k + 1) * 64];
           unrolled<0, 2>([&](auto sc) {
             constexpr int s = sc;
-            const half8v kk = halves_of(key.r[s][k]);
             if constexpr (I8) {
+              uint4& w = key.w[s][k >> 1];
+              // 64 values came as 16 a lane; lanes 0..31 hold the first block's, the others
+              // the second's.  Trading halves gives every lane eight of each block.
+              if constexpr (k % 2 == 0 && k + 1 < NB) {
+                trade_halves(w.x, w.z);
+                trade_halves(w.y, w.w);
+              }
+              const half8v kk = halves_of(k % 2 == 0 ? make_uint2(w.x, w.y) : make_uint2(w.z, w.w));
               const float4v part = mfma(kk, lo_, mfma(kk, hi, zero));
               unrolled<0, 4>([&](auto ic) {
                 constexpr int i = ic;
                 acc[s][i] += scaled(row_bcast<(k & 1) * 8 + 4 * s + i>(key.s[k >> 1]), part[i]);
               });
             } else {
+              const half8v kk = halves_of(key.w[s][k]);
               acc[s] = mfma(kk, hi, acc[s]);
               low[s] = mfma(kk, lo_, low[s]);
             }
