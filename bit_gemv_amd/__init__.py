@@ -398,18 +398,22 @@ def _rows(t, T: int, width: int, name: str):
         raise ValueError(f"{name} must live on the GPU (got {t.device})")
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be torch.float32 (got {t.dtype})")
-    shape, strides = t.shape, t.stride()
-    if len(shape) < 2 or shape[0] < T:
-        raise ValueError(f"{name} must have {T} or more rows (shape {tuple(shape)})")
-    row = 1
-    for n, s in zip(shape[:0:-1], strides[:0:-1]):
-        if n != 1 and s != row:
-            row = -1
-            break
-        row *= n
+    if t.dim() < 2 or t.shape[0] < T:
+        raise ValueError(f"{name} must have {T} or more rows (shape {tuple(t.shape)})")
+    if t.is_contiguous():
+        row = t.numel() // t.shape[0]
+        stride = row
+    else:
+        row = 1
+        for n, s in zip(t.shape[:0:-1], t.stride()[:0:-1]):
+            if n != 1 and s != row:
+                row = -1
+                break
+            row *= n
+        stride = t.stride(0)
     if row < width:
         raise ValueError(f"a row of {name} must be {width} or more contiguous values")
-    return t.data_ptr(), strides[0] if T > 1 else width
+    return t.data_ptr(), stride if T > 1 else width
 
 
 def rfp2_rope_freqs(rot: int, base: float, factor: float, orig_len: float, low_turns: float,
