@@ -7,7 +7,10 @@
 // workgroup takes eight tokens at once: where they fill one such group of the
 // cache (a prompt's tokens do), a lane holds four values of all eight and stores
 // or loads 32 (int8) or 64 (half) consecutive bytes; tokens that do not (a decode
-// step's belong to different sequences) are stored value by value.
+// step's belong to different sequences) are stored value by value.  20011 int8
+// tokens of 8 heads of 128 are read back in 36 us (5.8 TB/s; 73 us with a token a
+// workgroup and ordinary stores); 48 tokens are rotated and written in 4.6 us, where
+// the launch and the chain position, page, store are the time.
 #include <hip/hip_fp16.h>
 
 #include "kv_device.h"
@@ -18,9 +21,11 @@ namespace rfp2 {
 namespace {
 
 constexpr int kThreads = 256;
-// Tokens from which a workgroup takes eight of them: below, one each, which
-// spreads a decode step over more compute units.
-constexpr int64_t kGroupTokens = 512;
+// Tokens from which a workgroup takes eight of them: below, one each, a shorter chain in
+// more workgroups (write and read-back of 16 query and 8 key/value heads of 128: 700
+// tokens 16.6 against 26.6 us, 1500 tokens 26.4 against 29.7; 4001 tokens 69.8 against
+// 39.4, where one token a workgroup writes every line of the values in eight pieces).
+constexpr int64_t kGroupTokens = 2048;
 
 // Where the tokens of a workgroup lie in the cache.
 template <int TG>
@@ -64,17 +69,19 @@ __device__ __forceinline__ int64_t first_token(const int32_t* pos, int64_t block
   return TG == 1 ? block : block * TG - (pos[0] & 7);
 }
 
-// Code and scale as quantize_acts_kernel computes them, of four of the eight
-// lanes' 32 values.
+// Code and scale as quantize_acts_kernel computes them, of four of the eight lanes' 32
+// values.  Magnitudes are compared as integers, where infinities and NaN are the largest.
 __device__ __forceinline__ float quantize4(const float (&x)[4], uint32_t& codes) {
-  float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-  int finite = isfinite(x[0]) && isfinite(x[1]) && isfinite(x[2]) && isfinite(x[3]);
+  uint32_t top = 0;
 #pragma unroll
-  for (int off = 4; off >= 1; off >>= 1) {
-    amax = fmaxf(amax, __shfl_xor(amax, off, 64));
-    finite &= __shfl_xor(finite, off, 64);
-  }
-  const float scale = finite ? __fdiv_rn(amax, 127.0f) : __builtin_nanf("");
+  for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  // over the eight lanes: neighbours, pairs, then the other four in reverse
+  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true));
+  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, true));
+  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x141, 0xF, 0xF, true));
+  const bool finite = top < 0x7F800000u;
+  const float scale =
+      finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : __builtin_nanf("");
   codes = 0;
   if (finite && scale != 0.0f) {
 #pragma unroll
@@ -98,33 +105,34 @@ __device__ __forceinline__ void load4(float (&x)[4], const float* p) {
   x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
 
-// The four values from d on of a head at `src`, turned.
+// The four values x from d on of a head at `src`, turned.
 __device__ __forceinline__ void turn4(float (&x)[4], const float* src, int d, const RopeView& r,
                                       const double2* table) {
   const int half = r.rot >> 1;
   if (d >= r.rot) return;
   if (r.interleaved) {
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      if (d + i < r.rot) {
-        const float2 o = rope_turn(x[i], x[i + 1], table[(d + i) >> 1]);
-        x[i] = o.x;
-        x[i + 1] = o.y;
-      }
+    const double2 c0 = table[d >> 1], c1 = table[min((d >> 1) + 1, half - 1)];
+    const float2 a = rope_turn(x[0], x[1], c0), b = rope_turn(x[2], x[3], c1);
+    x[0] = a.x;
+    x[1] = a.y;
+    if (d + 2 < r.rot) {
+      x[2] = b.x;
+      x[3] = b.y;
     }
   } else if ((half & 3) == 0) {             // the four partners lie together too
+    const bool first = d < half;
+    const double2* cs = table + (first ? d : d - half);
     float o[4];
-    load4(o, src + (d < half ? d + half : d - half));
+    load4(o, src + (first ? d + half : d - half));
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      x[i] = d < half ? rope_turn(x[i], o[i], table[d + i]).x
-                      : rope_turn(o[i], x[i], table[d + i - half]).y;
+    for (int i = 0; i < 4; ++i) x[i] = rope_value(x[i], o[i], cs[i], first);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = d + i;
-      if (e < half) x[i] = rope_turn(x[i], src[e + half], table[e]).x;
-      else if (e < r.rot) x[i] = rope_turn(src[e - half], x[i], table[e - half]).y;
+      const bool first = e < half;
+      if (e < r.rot)
+        x[i] = rope_value(x[i], src[first ? e + half : e - half], table[first ? e : e - half], first);
     }
   }
 }

@@ -9,19 +9,21 @@
 // from keeping it streaming.
 //
 // Rows.  The new_tokens * H / kv_heads query rows of one (sequence, key/value
-// head) are taken together, 16 to a matrix tile; RW tiles (1, 2 or 4) go to
-// different waves of a workgroup, 4 / RW waves take every 4/RW-th tile of
-// tokens.  Rows past 16 * RW are further items that read the cache again.
+// head) are taken together: up to 16 a wave, in Q groups of four, and RW waves of a
+// workgroup (1, 2 or 4) take different rows of the same tokens.  The 4 / RW waves
+// that share their rows take every 4/RW-th tile of tokens.  Rows past 4 Q RW (64 at
+// most) are further items that read the cache again.
 //
 // Tokens.  A tile is 32 cached tokens.  Scores are S = K q^T with
-// v_mfma_f32_16x16x32_f16 (16 tokens x 32 values of a head x 16 rows), the sums
-// O^T = V^T P^T with v_mfma_f32_16x16x4_f32 (16 values x 4 tokens x 16 rows).
-// Row r of the first product's tile s stands for token 8 (r / 4) + 4 s + r % 4,
-// which leaves a lane with the scores of eight consecutive tokens 8g .. 8g+7
-// (g = lane / 16) of one query row (lane % 16): just what the second product
-// takes as its operand, four tokens 8g + j at a step, so the weights never leave
-// their registers.  Its other operand is eight tokens of one value, which the
-// cache's layout keeps side by side.
+// v_mfma_f32_16x16x32_f16 (16 tokens x 32 values of a head x 16 rows); the sums
+// O = W V with v_mfma_f32_4x4x1_f32, sixteen products of 4 rows x 1 token x 4
+// values at once.  Row r of the first product's tile s stands for token
+// 8 (r / 4) + 4 s + r % 4, which gives a lane the scores of eight consecutive tokens
+// 8g .. 8g+7 (g = lane / 16) of one query row (lane % 16).  The weights change
+// lanes through LDS (2 KB a wave at most); a lane of the second product holds one
+// value of eight tokens, which the cache's layout keeps side by side, so neither
+// product moves cached data between lanes (int8 keys trade halves once, to be
+// loaded 16 bytes at a time).
 //
 // Precision.  Scores, weights and sums are fp32.  The query enters the first
 // product as two halves, x = hi + lo (22 bits), scaled by a power of two a row;
@@ -30,16 +32,25 @@
 // exact operands.  A block of 32 values is one instruction long, so a key's scale
 // multiplies its block's partial score, and a value's scale the weight.  Weights
 // span more powers of two than halves hold (the largest may meet a value of 0),
-// so the second product is fp32: 64 instructions of 32 clocks a tile of 128
-// values, 16 bytes of an int8 cache a clock and compute unit against the 9 that
-// memory delivers.
+// so the second product is fp32.  The 4 x 4 form makes that affordable: it does
+// no work for rows that do not exist (with 16-row fp32 products the same kernel
+// took 400 us where it takes 330, at 128 sequences of up to 8000 tokens and four
+// rows a head).
 //
 // Split over the length.  The tiles of all (sequence, head) items form one line,
-// cut into equal shares, one a workgroup: a long sequence is spread over all
+// each item with a few tiles' worth in front for what starting on it costs, cut
+// into equal shares, one a workgroup: a long sequence is spread over all
 // workgroups, short ones are packed, whatever the lengths, which only the GPU
 // knows.  A share starts and ends inside an item at most once each: two slots of
 // unfinished sums a workgroup in the workspace, which a second kernel joins;
 // items inside one share are written out directly.
+//
+// What it reaches (MI355X; a plain read of 1 GiB runs at 6.44 TB/s): 128 sequences
+// of 3000 to 8000 tokens, 32 query and 8 key/value heads of 128, int8 cache, 1.63 GB:
+// 290 us, 5.6 TB/s, with 1.02 times the bytes read from memory that it cannot do
+// without; one of 131001 tokens, 64 query heads: 72 us, 4.2 TB/s (start and join are
+// about 12 us of it).  At 40 query rows a head (five new tokens) the fp32 products
+// bound it: 94 us where the transfer alone would take 29.
 #pragma once
 
 #include <hip/hip_fp16.h>

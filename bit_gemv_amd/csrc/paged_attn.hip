@@ -11,7 +11,10 @@ int item_rows(int64_t rows) {
   return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
 }
 
-// Rows up to which the join gives each a workgroup for every 32 values.
+// Rows up to which the join gives each a workgroup for every 32 values: one sequence of
+// 4097 tokens (32 rows) 14.2 us in all against 15.5 with a wave a row, of 131001 tokens
+// (64 rows) 77.5 against 80.9; 24 sequences (768 rows) 44.5 against 41.7, 128 sequences
+// (4096 rows) 316 against 297.
 constexpr int64_t kWideJoinRows = 256;
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }

@@ -445,8 +445,9 @@ rfp2_status rfp2_kv_read(const rfp2_kv_cache* cache, int64_t T, const int32_t* s
  *     y = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q.k_j - max).
  *   q   [B][new_tokens] rows of H heads of head_dim fp32 values, row i at
  *       q + i * q_stride; 16-byte aligned.
- *   y   [B][new_tokens][H][head_dim] fp32, 16-byte aligned.  A query that sees
- *       nothing (lens[b] <= 0, or a position below 0) gives zeros.
+ *   y   [B][new_tokens][H][head_dim] fp32, 16-byte aligned, no overlap with q
+ *       or the cache.  A query that sees nothing (lens[b] <= 0, or a position
+ *       below 0) gives zeros.
  *   lens [B] int32 on the device; 4-byte aligned.
  *   err nullable device int32: a length beyond max_pages * page_size, or a
  *       visible token on a page outside the cache, gives NaN rows, and 1 is

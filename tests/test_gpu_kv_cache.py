@@ -71,7 +71,8 @@ CASES = [  # T, H, D, P, first position, sequences
     (77, 3, 64, 8, 5, 1), (77, 1, 256, 32, 30, 1), (200, 2, 160, 128, 0, 2), (129, 4, 224, 16, 7, 3),
     # eight tokens a workgroup: starting inside a group of the cache, ending inside one, and
     # tokens that do not lie together
-    (515, 2, 64, 16, 5, 1), (1024, 1, 256, 64, 0, 1), (700, 3, 96, 8, 3, 3), (513, 1, 32, 128, 127, 1),
+    (2051, 2, 64, 16, 5, 1), (2048, 1, 256, 64, 0, 1), (2100, 3, 96, 8, 3, 3), (2049, 1, 32, 128, 127, 1),
+    (600, 2, 128, 64, 3, 1),
 ]
 
 
@@ -108,7 +109,7 @@ def test_write_and_read_back(fmt, T, H, D, P, first, seqs):
 
 
 @pytest.mark.parametrize("fmt", [rf.KV_F16, rf.KV_I8])
-@pytest.mark.parametrize("T", [37, 557])
+@pytest.mark.parametrize("T", [37, 2057])
 @pytest.mark.parametrize("rot,inter", [(64, False), (64, True), (38, False), (38, True), (2, True), (62, False)])
 def test_fused_equals_the_separate_calls(fmt, rot, inter, T):
     announce("rope_kv_write", fmt, rot, inter, T)

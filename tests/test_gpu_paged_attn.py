@@ -222,6 +222,39 @@ def test_non_finite_inputs_stay_in_their_rows(fmt):
 
 
 @pytest.mark.parametrize("fmt", [F16, I8])
+@pytest.mark.parametrize("D", [64, 96])
+def test_hidden_non_finite_values_stay_hidden(fmt, D):
+    """NaN and infinities in values that some rows do not see: a later new token's, and a
+    token's that has left the window.  Rows that do see them get them."""
+    announce("paged_attn hidden non-finite", fmt, D)
+    s = Setup(fmt, [150, 200], 4, 4, 2, D, 16, seed=16)
+    window = 30
+    ref, tol = s.reference(window)
+    kinds = [np.nan, np.inf, -np.inf]
+    for at, first_blind, kind in ((147, 0, 0), (116, 1, 1), (148, 0, 2)):
+        v = np.ones((1, 2, D), np.float32)
+        v[0, :, 5] = kinds[kind]                              # value 5 of both heads
+        k = s.k[0][at:at + 1].astype(np.float32)
+        one = to_dev(np.array([at], np.int32))
+        rf.rfp2_kv_write(s.cache, to_dev(k), to_dev(v), 1, to_dev(np.zeros(1, np.int32)), one)
+        got = host(s.run(window))
+        for t in range(4):
+            pos = 146 + t
+            sees = pos - window < at <= pos
+            lost = slice(0, 32) if fmt == I8 else slice(5, 6)  # int8: the block's scale is NaN
+            if sees:
+                assert not np.isfinite(got[0, t, :, lost]).any(), (at, t)
+                if fmt == F16 and kind:
+                    assert (got[0, t, :, 5] == kinds[kind]).all(), (at, t)
+            else:
+                assert np.isfinite(got[0, t]).all(), (at, t)
+        # the other sequence, and the values of the first that nothing touched, hold
+        assert_close(got[1], ref[1], tol[1], at)
+        clean = np.ones((1, 2, D), np.float32)
+        rf.rfp2_kv_write(s.cache, to_dev(k), to_dev(clean), 1, to_dev(np.zeros(1, np.int32)), one)
+
+
+@pytest.mark.parametrize("fmt", [F16, I8])
 def test_bad_lengths_and_pages(fmt):
     announce("paged_attn bad pages", fmt)
     s = Setup(fmt, [100, 100, 100, 100], 1, 4, 2, 64, 16, seed=12)
