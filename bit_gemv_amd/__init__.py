@@ -121,7 +121,7 @@ def header_symbols() -> list[str]:
 def _stream(stream):
     import torch
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -398,19 +398,16 @@ def _rows(t, T: int, width: int, name: str):
         raise ValueError(f"{name} must live on the GPU (got {t.device})")
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be torch.float32 (got {t.dtype})")
-    if t.dim() < 2 or t.shape[0] < T:
-        raise ValueError(f"{name} must have {T} or more rows (shape {tuple(t.shape)})")
-    if t.is_contiguous():
-        row = t.numel() // t.shape[0]
-        stride = row
-    else:
-        row = 1
-        for n, s in zip(t.shape[:0:-1], t.stride()[:0:-1]):
-            if n != 1 and s != row:
-                row = -1
-                break
-            row *= n
-        stride = t.stride(0)
+    shape = t.shape
+    if len(shape) < 2 or shape[0] < T:
+        raise ValueError(f"{name} must have {T} or more rows (shape {tuple(shape)})")
+    stride, *inner = t.stride()
+    row = 1
+    for n, s in zip(shape[:0:-1], reversed(inner)):
+        if s != row and n != 1:
+            row = -1
+            break
+        row *= n
     if row < width:
         raise ValueError(f"a row of {name} must be {width} or more contiguous values")
     return t.data_ptr(), stride if T > 1 else width
