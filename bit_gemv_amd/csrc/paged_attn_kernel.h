@@ -155,9 +155,6 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
   constexpr bool HALF = NB % 2 != 0;        // and a chunk of 32
   constexpr int CA = C + (HALF ? 1 : 0);
   constexpr int ES = I8 ? 1 : 2;
-  // Wide heads of halves: no registers for a second tile's values, the next tile's are
-  // requested when this one's have been used.
-  constexpr bool LATE = !I8 && NB >= 7;
   using Reg = std::conditional_t<I8, uint2, uint4>;   // eight codes or halves
   __shared__ uint32_t cum[kMaxAttnSeqs + 1];
   __shared__ int32_t len_of[kMaxAttnSeqs];
@@ -289,7 +286,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
       Reg r[4][C > 0 ? C : 1], h[2];
       float s[NW];
       bool bad;
-    } va, vb;
+    } v;
 
     // the page of token group `grp` (eight tokens), -1 where there is none
     auto page_of = [&](int grp) -> int32_t {
@@ -328,7 +325,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
           key.s[w] = a.c.ks[rs * NB + 16 * w + (2 * w + 1 < NB ? n : (n & 7))];
       }
     };
-    auto load_v = [&](Values& v, int tile, int32_t page) {
+    auto load_v = [&](int tile, int32_t page) {
       v.bad = !is_page(page);
       int64_t r[4];                         // the four token groups, the same for all lanes
 #pragma unroll
@@ -389,7 +386,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
       const int32_t pk1 = pk, pv1 = pv;
       next_pages(t + WT);
       load_k(tile0 + t, pk1, pv1);
-      load_v(va, tile0 + t, pv1);
+      load_v(tile0 + t, pv1);
     }
     float c;                                                // score -> base 2, unscaled
     {
@@ -429,7 +426,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
 
     // sum += V^T W of a tile, W in `weights` (transposed through LDS: a lane needs the
     // weights of row lane % 4 for one token, and holds one value of eight tokens)
-    auto add_products = [&](const Values& v, float4v (&sum)[CA][Q], auto scaled_by_s, auto&& of) {
+    auto add_products = [&](float4v (&sum)[CA][Q], auto scaled_by_s, auto&& of) {
       const float* w0 = &weights[wave][lane & 3][(lane >> 2) & 7];
       unrolled<0, 4>([&](auto uc) {
         constexpr int u = uc;
@@ -479,8 +476,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
       wave_fence();
     };
 
-    // One tile: its values lie in `v`, the next tile's go to `next`.
-    auto step = [&](Values& v, Values& next) {
+    for (; t < t1; t += WT) {
       const int tile = tile0 + t;
       // scores: x[4 s + i] of token 8 g + 4 s + i
       float x[8];
@@ -520,15 +516,17 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
           asm volatile("" : "+v"(x[j]));    // not put off until after the loads
         }
       }
-      // The next tile's keys and values are on their way while this one is worked on.  The
-      // pages after them are requested first: loads return in order.  The last tile
-      // requests itself again (out of the cache), because requests that only some
-      // iterations make would have to be waited for as if none had been made since.
+      // The next tile's keys are requested as soon as this one's have been used, and its
+      // values after this one's: one set of registers each (a second set for the values,
+      // requested here too, was slower: 98 against 94 us at five verified tokens, 295
+      // against 292 at 128 sequences).  The pages after them come first, since loads
+      // return in order.  The last tile requests itself again (out of the cache), because
+      // requests that only some iterations make would have to be waited for as if none
+      // had been made since.
       const int32_t pk1 = pk, pv1 = pv;
       const int ahead = tile0 + min(t + WT, last);
       next_pages(t + 2 * WT);
       load_k(ahead, pk1, pv1);
-      if constexpr (!LATE) load_v(next, ahead, pv1);
 
       // visibility: only a tile at an end of the sequence or of a window has hidden tokens
       const int pos0 = 32 * tile + 8 * g;
@@ -637,7 +635,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
               for (int k = 0; k < CA; ++k)
 #pragma unroll
                 for (int q = 0; q < Q; ++q) seen_of[k][q] = float4v{0.f, 0.f, 0.f, 0.f};
-              add_products(v, seen_of, std::false_type{}, of);
+              add_products(seen_of, std::false_type{}, of);
 #pragma unroll
               for (int k = 0; k < CA; ++k)
 #pragma unroll
@@ -660,17 +658,8 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
         }
       }
       put_weights(p);
-      add_products(v, o, std::bool_constant<I8>{}, [](float f) { return f; });
-      if constexpr (LATE) load_v(next, ahead, pv1);
-      t += WT;
-    };
-    while (t < t1) {
-      if constexpr (LATE) {
-        step(va, va);
-      } else {
-        step(va, vb);
-        if (t < t1) step(vb, va);
-      }
+      add_products(o, std::bool_constant<I8>{}, [](float f) { return f; });
+      load_v(ahead, pv1);
     }
 
     // ---- the waves' sums together, then out: finished, or into this share's slot
