@@ -68,11 +68,16 @@ constexpr int kAttnGroups = 3 * kAttnCus; // workgroups (shares) of a launch at 
 constexpr int kAttnItemStart = 8;         // tiles in whose time a workgroup starts on an item
 constexpr int kAttnMinTiles = 4;          // tiles of a share at least
 
-// Waves a SIMD that a variant's registers allow without spilling (as the compiler
-// reported them; nb: blocks of 32 values of a head, q: groups of four query rows).
+// Waves a SIMD, of those that a variant's registers allow without spilling (nb: blocks of
+// 32 values of a head, q: groups of four query rows).  More waves are also more shares to
+// start and to join, and pay only where they hide much: codes in heads of up to 128 gain
+// from the third (128 sequences 294 against 295 us, 32 sequences of 64 values 75 against
+// 78), halves lose (32 + 8 heads of 128, 4 sequences of 2000 to 6000 tokens: 25.8 us with
+// three, 23.4 with two; 32 sequences: 105 and 102).  A third wave for codes in heads of 256 (64
+// sequences: 70 us -> 83) and a second for 256 halves and eight rows (55 -> 58) lose too.
 constexpr int attn_waves(bool i8, int nb, int q) {
   if (i8) return nb <= 4 || (nb <= 6 && q == 1) ? 3 : nb <= 7 || q <= 2 ? 2 : 1;
-  return nb <= 4 ? (q == 1 ? 3 : 2) : (nb <= 6 && q <= 2) || q == 1 ? 2 : 1;
+  return nb <= 4 || (nb <= 6 && q <= 2) || q == 1 ? 2 : 1;
 }
 
 // a / b for a >= 0, b > 0: by way of a reciprocal while the numbers are small (the full
