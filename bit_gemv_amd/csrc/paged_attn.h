@@ -47,10 +47,10 @@
 //
 // What it reaches (MI355X; a plain read of 1 GiB runs at 6.44 TB/s): 128 sequences
 // of 3000 to 8000 tokens, 32 query and 8 key/value heads of 128, int8 cache, 1.63 GB:
-// 288 us, 5.7 TB/s, with 1.02 times the bytes read from memory that it cannot do
-// without; one of 131001 tokens, 64 query heads: 72 us, 4.2 TB/s (start and join are
+// 284 us, 5.7 TB/s, with 1.02 times the bytes read from memory that it cannot do
+// without; one of 131001 tokens, 64 query heads: 67 us, 4.5 TB/s (start and join are
 // about 12 us of it).  At 40 query rows a head (five new tokens) the fp32 products
-// bound it: 94 us where the transfer alone would take 29.
+// bound it: 90 us where the transfer alone would take 29.
 #pragma once
 
 #include <hip/hip_fp16.h>

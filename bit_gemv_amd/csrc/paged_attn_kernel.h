@@ -720,7 +720,8 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
 // The variant goes by the query rows of an item: as few groups of four as hold them, since
 // the fp32 products are done for whole groups (four rows in one group instead of four at
 // 128 sequences: 330 instead of 400 us); beyond 16 rows two or four waves share a tile's
-// rows, twelve each up to 48 (40 rows on four waves of twelve 94 us, of sixteen 109).
+// rows, twelve each up to 48 (40 rows on four waves of twelve 90 us; before the last
+// steps, 94 against 109 on waves of sixteen).
 template <bool I8, int NB>
 hipError_t launch_attn(const AttnArgs& a, int rows, int grid, hipStream_t stream) {
   const auto kernel = rows <= 4    ? paged_attn_kernel<I8, NB, 1, 1>
