@@ -4,12 +4,16 @@
 //
 // Pair i of a head turns by the angle pos * f_i.  In fp32 the angle of
 // position 10^6 is off by 2^-24 * 10^6 = 0.06 radians, so it is formed in
-// fp64 and reduced to a fraction of a turn there; cosine, sine and the
-// rotation itself stay in fp64 too and the rotated value is rounded to fp32
-// once.  That makes the value reproducible (it is the correctly rounded one
-// but for ~2^-28 of the cases), which matters where it is quantized to int8
-// next: a last-bit difference would flip codes.  The fp64 work is one sincos
-// per pair and token and four multiplications and additions per pair and
+// fp64 and reduced to a fraction of a turn there; the product and 1 / (2 pi)
+// are held in two numbers each, since one rounding of the number of turns is
+// 2^-53 of ALL turns: at position 2^31 a whole last place of fp32, at 10^6 still
+// enough to round one value in a thousand the other way.  So the fraction is off by
+// a few units of 2^-53 at any position.  Cosine, sine and the rotation itself stay in
+// fp64 too and the rotated value is rounded to fp32 once.  That makes the value
+// reproducible (it is the correctly rounded one but where the exact value lies
+// within some 2^-50 of the pair's size of the border), which matters where it is
+// quantized to int8 next: a last-bit difference would flip codes.  The fp64 work is one
+// sincos per pair and token and four multiplications and additions per pair and
 // head, under the time of the transfer: 4096 tokens of 40 heads of 128 values are
 // rotated in 26 us, 6.4 TB/s read and written.
 #pragma once
@@ -20,10 +24,15 @@ namespace rfp2 {
 
 // mscale * (cos, sin) of pair i's angle at position pos.
 __device__ __forceinline__ double2 rope_entry(const RopeView& r, int32_t pos, int i) {
-  double turns = (double)pos * r.freqs[i] * 0.15915494309189533577;   // 1 / (2 pi)
-  turns -= rint(turns);
+#pragma clang fp contract(off)              // `turns` is the rounded product wherever it stands
+  // 1 / (2 pi) = hi + lo
+  constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  const double f = r.freqs[i], p = (double)pos;
+  const double a = p * f, a_lo = __builtin_fma(p, f, -a);
+  const double turns = a * hi;
+  const double rest = __builtin_fma(a, hi, -turns) + __builtin_fma(a, lo, a_lo * hi);
   double s, c;
-  sincospi(2.0 * turns, &s, &c);
+  sincospi(2.0 * ((turns - rint(turns)) + rest), &s, &c);
   return make_double2(r.mscale * c, r.mscale * s);
 }
 

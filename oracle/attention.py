@@ -7,6 +7,7 @@ keeps it.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import numpy as np
@@ -90,3 +91,38 @@ def attention(q, k, v, pos, scale, window=0):
         mag[h] = w @ np.abs(vv) / w.sum()
         big[h] = abs(scale) * (np.abs(kk) @ np.abs(q[h])).max()
     return y, mag, big
+
+
+@functools.lru_cache
+def _pi_in_bits(bits):
+    """pi * 2^bits, by Machin's formula in whole numbers."""
+    one = 1 << (bits + 32)
+
+    def arctan_of_one_over(x):
+        term, total, n = one // x, 0, 1
+        while term:
+            total += term // n if n % 4 == 1 else -(term // n)
+            term //= x * x
+            n += 2
+        return total
+    return 4 * (4 * arctan_of_one_over(5) - arctan_of_one_over(239)) >> 32
+
+
+def turn_fraction(pos, f):
+    """pos * f radians as a fraction of a turn in [-1/2, 1/2], rounded once: the product
+    and its division by 2 pi are whole-number arithmetic, however far the position."""
+    num, den = float(f).as_integer_ratio()
+    bits = 256
+    turns = (int(pos) * num << (2 * bits)) // (den * 2 * _pi_in_bits(bits))   # * 2^bits
+    rest = turns & ((1 << bits) - 1)
+    if rest >> (bits - 1):
+        rest -= 1 << bits
+    return rest / (1 << bits)
+
+
+def rope_far(x, pos, freqs, rot, interleaved, mscale=1.0):
+    """`rope` with the angles of `turn_fraction`: for positions where the product
+    pos * f no longer fits 53 bits well enough."""
+    a = np.array([[2.0 * math.pi * turn_fraction(p, f) for f in freqs] for p in pos])
+    return np.concatenate([rope(x[t:t + 1], [1], a[t], rot, interleaved, mscale)
+                           for t in range(len(a))])

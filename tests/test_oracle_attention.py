@@ -81,3 +81,19 @@ def test_attention_sees_nothing_gives_zeros():
     q, k, v = np.ones((2, 8)), np.ones((0, 1, 8)), np.ones((0, 1, 8))
     assert not oa.attention(q, k, v, -1, 1.0)[0].any()
     assert not oa.attention(q, np.ones((3, 1, 8)), np.ones((3, 1, 8)), -1, 1.0)[0].any()
+
+
+def test_turn_fractions_of_far_positions():
+    assert abs(oa.turn_fraction(355, 1.0) - (355 / (2 * math.pi) - 57)) < 1e-13
+    assert oa.turn_fraction(0, 0.3) == 0.0 and oa.turn_fraction(-5, 0.3) == -oa.turn_fraction(5, 0.3)
+    # fractions add up modulo one, however far: p f = (p - 1) f + f
+    for p in (1 << 20, (1 << 31) - 1, -(1 << 31)):
+        for f in (1.0, 0.7498942093324559, 1e-4):
+            d = oa.turn_fraction(p, f) - oa.turn_fraction(p - 1, f) - oa.turn_fraction(1, f)
+            assert abs(d - round(d)) < 4e-16, (p, f, d)
+    # and near the start both forms are the same rotation
+    x = np.random.default_rng(3).standard_normal((4, 2, 16)).astype(np.float32)
+    f = oa.rope_freqs(16, 10000.0)
+    for i in (False, True):
+        assert np.allclose(oa.rope(x, [0, 1, 2, 9], f, 16, i), oa.rope_far(x, [0, 1, 2, 9], f, 16, i),
+                           rtol=0, atol=1e-14)
