@@ -70,14 +70,23 @@ __device__ __forceinline__ half8v halves_of(uint4 x) {
 
 // x = hi + lo, both halves, cut off (not rounded: one packed instruction each);
 // what remains is below 2^-20 of x, and below 2^-24 absolutely.
+// MEETS_INF: the other operand may be infinite (a half key), where a part of 0 would make
+// NaN of a product that is infinite.  So neither part of an x that is not 0 is 0: one that
+// would be is the smallest half of x's sign, 2^-24 (2^-37 of the row's largest value).
+template <bool MEETS_INF>
 __device__ __forceinline__ void split8(const float (&x)[8], half8v& hi, half8v& lo) {
   union { half2v h[4]; half8v v; } a, b;
+  auto least = [](float part, float x) {
+    if constexpr (!MEETS_INF) return part;
+    return x != 0.0f && fabsf(part) < 0x1p-24f ? copysignf(0x1p-24f, x) : part;
+  };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    a.h[i] = __builtin_bit_cast(half2v, __builtin_amdgcn_cvt_pkrtz(x[2 * i], x[2 * i + 1]));
-    b.h[i] = __builtin_bit_cast(
-        half2v, __builtin_amdgcn_cvt_pkrtz(__builtin_fmaf((float)a.h[i].x, -1.0f, x[2 * i]),
-                                           __builtin_fmaf((float)a.h[i].y, -1.0f, x[2 * i + 1])));
+    const float x0 = x[2 * i], x1 = x[2 * i + 1];
+    a.h[i] = __builtin_bit_cast(half2v, __builtin_amdgcn_cvt_pkrtz(least(x0, x0), least(x1, x1)));
+    const float l0 = __builtin_fmaf((float)a.h[i].x, -1.0f, x0);
+    const float l1 = __builtin_fmaf((float)a.h[i].y, -1.0f, x1);
+    b.h[i] = __builtin_bit_cast(half2v, __builtin_amdgcn_cvt_pkrtz(least(l0, x0), least(l1, x1)));
   }
   hi = a.v;
   lo = b.v;
@@ -402,14 +411,13 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
       const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
+        if (k % WT != wt) continue;         // the waves of one row tile hold the same: shared out
 #pragma unroll
         for (int i = 0; i < 8; ++i) qx[k][i] *= up;
         half8v hi, lo_;
-        split8(qx[k], hi, lo_);
-        if (wt == 0) {                      // (the waves of one row tile hold the same)
-          sh.queries[wr][k][0][lane_q] = hi;
-          sh.queries[wr][k][1][lane_q] = lo_;
-        }
+        split8<!I8>(qx[k], hi, lo_);
+        sh.queries[wr][k][0][lane_q] = hi;
+        sh.queries[wr][k][1][lane_q] = lo_;
       }
       c = a.scale * 1.44269504088896340736f * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
     }
