@@ -545,11 +545,13 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
         for (int j = 0; j < 8; ++j) x[j] = __builtin_nanf("");
         if (a.err) *a.err = 1;
       }
+      // (a token's own score may be minus infinity too: what a row sees goes by positions)
+      const int from = a.window > 0 ? row_pos - a.window + 1 : 0;
+      auto sees = [&](int j) { return pos0 + j <= row_pos && pos0 + j >= from; };
       if (edge) {
-        const int from = a.window > 0 ? row_pos - a.window + 1 : 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (pos0 + j > row_pos || pos0 + j < from) x[j] = -INFINITY;
+          if (!sees(j)) x[j] = -INFINITY;
         if constexpr (I8) {
           // scales of tokens that no row sees may hold anything
 #pragma unroll
@@ -564,7 +566,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
             const int lane_o = here(threadIdx.x) & 63, g_o = lane_o >> 4;
             uint32_t seen = 0, lost = 0;                     // tokens; blocks
 #pragma unroll
-            for (int j = 0; j < 8; ++j) seen |= (x[j] != -INFINITY ? 1u : 0u) << j;
+            for (int j = 0; j < 8; ++j) seen |= (sees(j) ? 1u : 0u) << j;
 #pragma unroll
             for (int k = 0; k < NB; ++k)
               if ((uint32_t)(odd[k >> 1] >> (16 * g_o + 8 * (k & 1))) & seen) lost |= 1u << k;
@@ -635,7 +637,7 @@ __global__ __launch_bounds__(kAttnThreads, attn_waves(I8, NB, Q)) void paged_att
           if (__any(odd)) {
             float seen[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) seen[j] = x[j] == -INFINITY ? 0.0f : 1.0f;
+            for (int j = 0; j < 8; ++j) seen[j] = sees(j) ? 1.0f : 0.0f;
             put_weights(seen);
             auto count = [&](float inf, auto&& of) {
               float4v seen_of[CA][Q];
