@@ -26,6 +26,9 @@ constexpr int kThreads = 256;
 // tokens 16.6 against 26.6 us, 1500 tokens 26.4 against 29.7; 4001 tokens 69.8 against
 // 39.4, where one token a workgroup writes every line of the values in eight pieces).
 constexpr int64_t kGroupTokens = 2048;
+// Tokens of a launch, eight to a workgroup (two more where they do not line up): a launch
+// holds 2^32 threads at most, so more tokens take several.
+constexpr int64_t kLaunchTokens = 8 * (kMaxGrid - 2);
 
 // Where the tokens of a workgroup lie in the cache.
 template <int TG>
@@ -371,7 +374,6 @@ hipError_t launch_kv_write(const KvView& c, bool i8, const float* q, const float
                            int64_t q_out_stride, int32_t* err, hipStream_t stream) {
   const bool wide = T >= kGroupTokens;
   const int heads = (int)H + 2 * c.heads;
-  const int64_t blocks = wide ? T / 8 + 2 : T;
   // A workgroup takes one pass of its threads over the heads (eight heads of 128
   // values), and computes the angles of its tokens for itself: at 4001 tokens of 32 heads
   // the write and read-back take 41 us, 54 us with half the heads a workgroup and 64 us
@@ -379,10 +381,17 @@ hipError_t launch_kv_write(const KvView& c, bool i8, const float* q, const float
   const int per = kThreads / (c.dim / 4);
   const auto kernel = wide ? (i8 ? kv_write_kernel<true, 8> : kv_write_kernel<false, 8>)
                            : (i8 ? kv_write_kernel<true, 1> : kv_write_kernel<false, 1>);
-  hipLaunchKernelGGL(kernel, dim3((uint32_t)blocks, (uint32_t)((heads + per - 1) / per)),
-                     dim3(kThreads), 0, stream, c, q, k, v, T, (int)H, q_stride, k_stride,
-                     v_stride, seq, pos, rope, q_out, q_out_stride, err, per);
-  return hipGetLastError();
+  for (int64_t t = 0; t < T; t += kLaunchTokens) {
+    const int64_t n = std::min(T - t, kLaunchTokens), blocks = wide ? n / 8 + 2 : n;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)blocks, (uint32_t)((heads + per - 1) / per)),
+                       dim3(kThreads), 0, stream, c, H ? q + t * q_stride : q, k + t * k_stride,
+                       v + t * v_stride, n, (int)H, q_stride, k_stride, v_stride, seq + t,
+                       pos + t, rope, H ? q_out + t * q_out_stride : q_out, q_out_stride, err,
+                       per);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_kv_read(const KvView& c, bool i8, int64_t T, const int32_t* seq,
@@ -391,9 +400,15 @@ hipError_t launch_kv_read(const KvView& c, bool i8, int64_t T, const int32_t* se
   const bool wide = T >= kGroupTokens;
   const auto kernel = wide ? (i8 ? kv_read_kernel<true, 8> : kv_read_kernel<false, 8>)
                            : (i8 ? kv_read_kernel<true, 1> : kv_read_kernel<false, 1>);
-  hipLaunchKernelGGL(kernel, dim3((uint32_t)(wide ? T / 8 + 2 : T)), dim3(kThreads), 0, stream, c,
-                     T, seq, pos, k, v, k_stride, v_stride, err);
-  return hipGetLastError();
+  for (int64_t t = 0; t < T; t += kLaunchTokens) {
+    const int64_t n = std::min(T - t, kLaunchTokens);
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)(wide ? n / 8 + 2 : n)), dim3(kThreads), 0, stream,
+                       c, n, seq + t, pos + t, k + t * k_stride, v + t * v_stride, k_stride,
+                       v_stride, err);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace rfp2

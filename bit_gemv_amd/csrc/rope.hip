@@ -135,9 +135,16 @@ hipError_t launch_rope(const float* x, int64_t T, int64_t H, int64_t D, int64_t 
       !v4    ? (inter ? rope_kernel<true, false, false> : rope_kernel<false, false, false>)
       : many ? (inter ? rope_kernel<true, true, true> : rope_kernel<false, true, true>)
              : (inter ? rope_kernel<true, true, false> : rope_kernel<false, true, false>);
-  hipLaunchKernelGGL(kernel, dim3((uint32_t)T, (uint32_t)((H + per - 1) / per)), dim3(kThreads),
-                     0, stream, x, (int)H, (int)D, x_stride, pos, rope, y, y_stride, per);
-  return hipGetLastError();
+  // One workgroup a token: a launch holds 2^32 threads at most, so more tokens take several.
+  for (int64_t t = 0; t < T; t += kMaxGrid) {
+    const int64_t n = std::min(T - t, kMaxGrid);
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)n, (uint32_t)((H + per - 1) / per)),
+                       dim3(kThreads), 0, stream, x + t * x_stride, (int)H, (int)D, x_stride,
+                       pos + t, rope, y + t * y_stride, y_stride, per);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace rfp2
