@@ -481,16 +481,19 @@ def rfp2_paged_attn_workspace_bytes(cache, B: int, new_tokens: int, H: int) -> i
 def rfp2_paged_attn(cache, q, B: int, new_tokens: int, H: int, lens, scale: float, y,
                     window: int = 0, err=None, workspace=None, stream=None) -> None:
     """q: [B, new_tokens, ...] or [B * new_tokens, ...], H * D contiguous values
-    a row, the rows evenly spaced; y: [B, new_tokens, H, D], contiguous.
+    a row, the rows evenly spaced (a buffer of more sequences is passed as q[:B]); y: [B, new_tokens, H, D], contiguous.
     workspace: a uint8 GPU tensor of at least rfp2_paged_attn_workspace_bytes
     bytes; when None, one is allocated for this call (on the current stream
     only: a call on another stream brings its own)."""
     import torch
     rows, width = B * new_tokens, H * cache.head_dim
-    if isinstance(q, torch.Tensor) and q.dim() > 2 and q.shape[0] == B and q.shape[1] == new_tokens:
-        if B > 1 and new_tokens > 1 and q.stride(0) != new_tokens * q.stride(1):
-            raise ValueError("the rows of q must be evenly spaced")
-        q = q[:, 0] if new_tokens == 1 else q[0] if B == 1 else q.view(rows, *q.shape[2:])
+    if isinstance(q, torch.Tensor) and q.dim() > 2 and q.shape[1] == new_tokens:
+        if q.shape[0] == B:
+            if B > 1 and new_tokens > 1 and q.stride(0) != new_tokens * q.stride(1):
+                raise ValueError("the rows of q must be evenly spaced")
+            q = q[:, 0] if new_tokens == 1 else q[0] if B == 1 else q.view(rows, *q.shape[2:])
+        elif q.shape[0] > B and new_tokens > 1 and q[0, 0].numel() >= width:
+            raise ValueError(f"q holds {q.shape[0]} sequences, not {B}: pass q[:{B}]")
     qp, qs = _rows(q, rows, width, "q")
     if workspace is None:
         if stream is not None:
