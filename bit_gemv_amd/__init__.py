@@ -481,7 +481,8 @@ def rfp2_paged_attn_workspace_bytes(cache, B: int, new_tokens: int, H: int) -> i
 def rfp2_paged_attn(cache, q, B: int, new_tokens: int, H: int, lens, scale: float, y,
                     window: int = 0, err=None, workspace=None, stream=None) -> None:
     """q: [B, new_tokens, ...] or [B * new_tokens, ...], H * D contiguous values
-    a row, the rows evenly spaced (a buffer of more sequences is passed as q[:B]); y: [B, new_tokens, H, D], contiguous.
+    a row, the rows evenly spaced (a buffer of more sequences is passed as q[:B]);
+    y: [B, new_tokens, H, D], contiguous.
     workspace: a uint8 GPU tensor of at least rfp2_paged_attn_workspace_bytes
     bytes; when None, one is allocated for this call (on the current stream
     only: a call on another stream brings its own)."""

@@ -399,8 +399,11 @@ typedef struct rfp2_kv_cache {
  *   err   nullable device int32: a token whose sequence, position or page lies
  *         outside the cache is not stored and 1 is written to *err (never
  *         cleared by the call).
- * RFP2_KV_F16 rounds to nearest even (beyond 65504: infinity).  Where two
- * tokens of a call name one place, either may remain.
+ * RFP2_KV_F16 rounds to nearest even (beyond 65504: infinity).
+ * A place should be named once in a call.  Named by several tokens it holds a
+ * mixture: each code, half or scale is one token's, but the scale of a block may
+ * be another's than its codes (nothing orders the stores).  Other places are not
+ * affected.
  * Requires T >= 1, strides >= kv_heads * head_dim and multiples of 4.
  */
 rfp2_status rfp2_kv_write(const rfp2_kv_cache* cache, const float* k, const float* v, int64_t T,
@@ -411,7 +414,8 @@ rfp2_status rfp2_kv_write(const rfp2_kv_cache* cache, const float* k, const floa
  * rfp2_rope_kv_write -- rfp2_rope of T tokens' H query heads and kv_heads key
  * heads at positions pos, and rfp2_kv_write of the rotated keys and of the
  * values, in one launch (the row of one QKV product: q, k and v may be parts
- * of the same rows).  Bit-identical to the separate calls.  q_out (row t at
+ * of the same rows).  Bit-identical to the separate calls (but for places named
+ * by several tokens, as in rfp2_kv_write).  q_out (row t at
  * q_out + t * q_out_stride) must not overlap q, k or v; it is written for
  * every token, padding too.  H == 0 with q == q_out == NULL rotates and
  * stores keys alone.
