@@ -436,12 +436,13 @@ def rfp2_rope(x, T: int, H: int, D: int, pos, freqs, rot: int, style: int, mscal
 
 def rfp2_kv_write(cache, k, v, T: int, seq, pos, err=None, stream=None) -> None:
     import torch
+    ref = _cache_ref(cache)
     row = cache.kv_heads * cache.head_dim
     kp, ks = _rows(k, T, row, "k")
     vp, vs = _rows(v, T, row, "v")
     errp = None if err is None else _ptr(err, torch.int32, 1, "err")
     _check("rfp2_kv_write", lib().rfp2_kv_write(
-        _cache_ref(cache), kp, vp, T, ks, vs, _ptr(seq, torch.int32, T, "seq"),
+        ref, kp, vp, T, ks, vs, _ptr(seq, torch.int32, T, "seq"),
         _ptr(pos, torch.int32, T, "pos"), errp, _stream(stream)))
 
 
@@ -449,6 +450,7 @@ def rfp2_rope_kv_write(cache, q, k, v, T: int, H: int, seq, pos, freqs, rot: int
                        mscale: float, q_out, err=None, stream=None) -> None:
     """q, q_out: T rows of H heads (both None with H == 0: keys alone)."""
     import torch
+    ref = _cache_ref(cache)
     row = cache.kv_heads * cache.head_dim
     qp, qs, op, os_ = None, 0, None, 0
     if H:
@@ -458,19 +460,20 @@ def rfp2_rope_kv_write(cache, q, k, v, T: int, H: int, seq, pos, freqs, rot: int
     vp, vs = _rows(v, T, row, "v")
     errp = None if err is None else _ptr(err, torch.int32, 1, "err")
     _check("rfp2_rope_kv_write", lib().rfp2_rope_kv_write(
-        _cache_ref(cache), qp, kp, vp, T, H, qs, ks, vs, _ptr(seq, torch.int32, T, "seq"),
+        ref, qp, kp, vp, T, H, qs, ks, vs, _ptr(seq, torch.int32, T, "seq"),
         _ptr(pos, torch.int32, T, "pos"), _ptr(freqs, torch.float64, rot // 2, "freqs"), rot,
         style, mscale, op, os_, errp, _stream(stream)))
 
 
 def rfp2_kv_read(cache, T: int, seq, pos, k, v, err=None, stream=None) -> None:
     import torch
+    ref = _cache_ref(cache)
     row = cache.kv_heads * cache.head_dim
     kp, ks = _rows(k, T, row, "k")
     vp, vs = _rows(v, T, row, "v")
     errp = None if err is None else _ptr(err, torch.int32, 1, "err")
     _check("rfp2_kv_read", lib().rfp2_kv_read(
-        _cache_ref(cache), T, _ptr(seq, torch.int32, T, "seq"),
+        ref, T, _ptr(seq, torch.int32, T, "seq"),
         _ptr(pos, torch.int32, T, "pos"), kp, vp, ks, vs, errp, _stream(stream)))
 
 
@@ -487,6 +490,7 @@ def rfp2_paged_attn(cache, q, B: int, new_tokens: int, H: int, lens, scale: floa
     bytes; when None, one is allocated for this call (on the current stream
     only: a call on another stream brings its own)."""
     import torch
+    ref = _cache_ref(cache)
     rows, width = B * new_tokens, H * cache.head_dim
     if isinstance(q, torch.Tensor) and q.dim() > 2 and q.shape[1] == new_tokens:
         if q.shape[0] == B:
@@ -503,7 +507,7 @@ def rfp2_paged_attn(cache, q, B: int, new_tokens: int, H: int, lens, scale: floa
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=y.device)
     errp = None if err is None else _ptr(err, torch.int32, 1, "err")
     _check("rfp2_paged_attn", lib().rfp2_paged_attn(
-        _cache_ref(cache), qp, B, new_tokens, H, qs, _ptr(lens, torch.int32, B, "lens"), scale,
+        ref, qp, B, new_tokens, H, qs, _ptr(lens, torch.int32, B, "lens"), scale,
         window, _ptr(y, torch.float32, rows * width, "y"), errp,
         _ptr(workspace, torch.uint8, 0, "workspace"), workspace.numel(), _stream(stream)))
 

@@ -6,8 +6,11 @@ import bit_gemv_amd as rf
 torch = pytest.importorskip("torch")
 
 
-class FakeCache:
+class FakeCache(rf.KvCache):
     head_dim = 64
+
+    def __init__(self):
+        self._struct = rf._KvCacheStruct()
 
 
 def call(q, B, T, H):
@@ -32,3 +35,15 @@ def test_a_buffer_of_more_sequences_is_refused(shape):
 def test_both_forms_reach_the_check_of_the_device(shape, B, T, H):
     with pytest.raises(ValueError, match="GPU"):
         call(torch.zeros(shape), B, T, H)
+
+
+def test_a_cache_that_is_none_is_a_type_error():
+    z = torch.zeros(2, 64)
+    for call_it in (lambda c: rf.rfp2_kv_write(c, z, z, 2, z, z),
+                    lambda c: rf.rfp2_rope_kv_write(c, z, z, z, 2, 1, z, z, z, 64, 0, 1.0, z),
+                    lambda c: rf.rfp2_kv_read(c, 2, z, z, z, z),
+                    lambda c: rf.rfp2_paged_attn(c, z, 2, 1, 1, z, 0.1, z),
+                    lambda c: rf.rfp2_paged_attn_workspace_bytes(c, 2, 1, 1)):
+        for c in (None, z):
+            with pytest.raises(TypeError, match="KvCache"):
+                call_it(c)
