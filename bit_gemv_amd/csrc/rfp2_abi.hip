@@ -314,6 +314,7 @@ rfp2_status rfp2_rope_kv_write(const rfp2_kv_cache* cache, const float* q, const
   if (H > 0 && (!row_stride_ok(q_stride, H * c.dim) || !row_stride_ok(q_out_stride, H * c.dim)))
     return RFP2_E_SHAPE;
   if (!aligned(freqs, 8) || !aligned(q, 16) || !aligned(q_out, 16)) return RFP2_E_ALIGN;
+  if (H > 0 && (q_out == q || q_out == k || q_out == v)) return RFP2_E_SHAPE;
   (void)hipGetLastError();
   const rfp2::RopeView rope = {freqs, mscale, (int32_t)rot, style == RFP2_ROPE_INTERLEAVED};
   return from_hip(rfp2::launch_kv_write(c, cache->format == RFP2_KV_I8, q, k, v, T, H, q_stride,

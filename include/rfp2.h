@@ -416,7 +416,8 @@ rfp2_status rfp2_kv_write(const rfp2_kv_cache* cache, const float* k, const floa
  * values, in one launch (the row of one QKV product: q, k and v may be parts
  * of the same rows).  Bit-identical to the separate calls (but for places named
  * by several tokens, as in rfp2_kv_write).  q_out (row t at
- * q_out + t * q_out_stride) must not overlap q, k or v; it is written for
+ * q_out + t * q_out_stride) must not overlap q, k or v (equal to one of them it is
+ * refused: lanes read their pairs while others write); it is written for
  * every token, padding too.  H == 0 with q == q_out == NULL rotates and
  * stores keys alone.
  * Requires what the two calls require, and rot <= head_dim.
