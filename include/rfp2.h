@@ -461,7 +461,11 @@ rfp2_status rfp2_kv_read(const rfp2_kv_cache* cache, int64_t T, const int32_t* s
  *       B, new_tokens, H) bytes, 256-byte aligned, owned by the caller;
  *       overwritten.  Calls that share a workspace must not overlap in time.
  * Scores, weights and sums are held in fp32; the queries enter the matrix
- * cores as two half-precision numbers each (22 bits of the row's largest).  The result
+ * cores as two half-precision numbers each (22 bits of the row's largest), scaled by a
+ * power of two: scores and sums stay finite for int8 keys up to 2^104 and values up to
+ * 2^87 in magnitude (halves end far below), beyond which results may be infinite or NaN.
+ * A score of minus infinity (a half key beyond 65504) is a weight of 0, one of plus
+ * infinity makes its row NaN.  The result
  * depends on nothing but the arguments (no atomics on values) and is the same
  * from call to call.  What lies in the cache beyond a sequence's length never
  * reaches an output.  Nothing is read back to the host, so the call can be
