@@ -99,3 +99,28 @@ def test_range_of_an_int8_cache():
                      to_dev(np.arange(n, dtype=np.int32)))
     s.k, s.v = [oa.held(k, True)], [oa.held(v, True)]
     assert_close(host(s.run()), *s.reference())
+
+
+@pytest.mark.parametrize("fmt", [F16, I8])
+@pytest.mark.parametrize("lens,T,H,Hkv", [([300], 1, 1024, 1024), ([300], 1, 600, 600), ([70], 8, 1024, 512),
+                                          ([40, 0, 9], 1, 1024, 1024)])
+def test_many_heads(fmt, lens, T, H, Hkv):
+    """As many (sequence, head) items as there are workgroups, and more of one sequence."""
+    announce("paged_attn many heads", fmt, lens, T, H, Hkv)
+    s = Setup(fmt, lens, T, H, Hkv, 32, 8, seed=H + T)
+    assert_close(host(s.run()), *s.reference())
+
+
+@pytest.mark.parametrize("fmt", [F16, I8])
+def test_first_sequences_of_a_larger_buffer(fmt):
+    """B below the cache's sequences, queries q[:B] of a buffer for all of them."""
+    announce("paged_attn part of a buffer", fmt)
+    s = Setup(fmt, [90, 33, 150, 20], 3, 4, 2, 64, 16, seed=21)
+    ref, tol = s.reference()
+    q = to_dev(s.q)
+    lens = to_dev(np.array(s.lens, np.int32))
+    y = torch.full((4, 3, 4, 64), -3.0, device=device())
+    rf.rfp2_paged_attn(s.cache, q[:2], 2, 3, 4, lens, s.scale, y)
+    got = host(y)
+    assert_close(got[:2], ref[:2], tol[:2])
+    assert (got[2:] == -3.0).all()
