@@ -25,6 +25,10 @@ constexpr int kThreads = 256;
 // more workgroups (write and read-back of 16 query and 8 key/value heads of 128: 700
 // tokens 16.6 against 26.6 us, 1500 tokens 26.4 against 29.7; 4001 tokens 69.8 against
 // 39.4, where one token a workgroup writes every line of the values in eight pieces).
+// Groups follow the call's first token (first_token): of several prompts in one call only
+// those that lie in step with it modulo 8 keep the wide stores of the values.  Writing two of
+// 2001 tokens takes 29.4 us over halves and 33.0 over codes, one of 4002 takes 26.1 and
+// 27.6; four of 1001 take 32.4 and 32.9, four of 1000 take 26.0 and 27.5.
 constexpr int64_t kGroupTokens = 2048;
 // Tokens of a launch, eight to a workgroup (two more where they do not line up): a launch
 // holds 2^32 threads at most, so more tokens take several.

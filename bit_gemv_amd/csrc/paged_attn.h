@@ -49,8 +49,11 @@
 // of 3000 to 8000 tokens, 32 query and 8 key/value heads of 128, int8 cache, 1.63 GB:
 // 284 us, 5.7 TB/s, with 1.02 times the bytes read from memory that it cannot do
 // without; one of 131001 tokens, 64 query heads: 67 us, 4.5 TB/s (start and join are
-// about 12 us of it).  At 40 query rows a head (five new tokens) the fp32 products
-// bound it: 90 us where the transfer alone would take 29.
+// about 12 us of it).  At 40 query rows a head (five new tokens, halves) it takes 90 us
+// where the transfer alone would take 29, and nothing is busy throughout: the matrix
+// cores 37 % of the clocks, the vector pipes 36 %.  They take turns: two waves a SIMD,
+// and a wave's products wait for its own conversions of the values to fp32 (64 a lane and
+// tile at heads of 128), its weights' way through LDS and the tile's loads.
 #pragma once
 
 #include <hip/hip_fp16.h>
