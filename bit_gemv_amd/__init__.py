@@ -21,6 +21,8 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "rfp2.h")
 KV_F16, KV_I8 = 0, 1
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ATTN_MAX_NEW = 8
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
+GATE_SILU, GATE_GELU = 0, 1
 
 RFP2_OK, RFP2_E_NULL, RFP2_E_SHAPE, RFP2_E_ALIGN, RFP2_E_LAUNCH = 0, -1, -2, -3, -4
 GEMV_MAX_M = 8
@@ -74,6 +76,17 @@ _SIGNATURES = {
     "rfp2_paged_attn_workspace_bytes": ([_c_cache, _c_i64, _c_i64, _c_i64], ctypes.c_size_t),
     "rfp2_paged_attn": ([_c_cache, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, ctypes.c_float,
                          _c_i64, _c_p, _c_p, _c_p, ctypes.c_size_t, _c_p], ctypes.c_int),
+    "rfp2_rms_norm": ([_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_f64, _c_p, _c_i64, _c_p],
+                      ctypes.c_int),
+    "rfp2_add_rms_norm": ([_c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_f64, _c_p, _c_i64,
+                           _c_p, _c_i64, _c_p, _c_p, _c_p], ctypes.c_int),
+    "rfp2_moe_combine": ([_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_f64, _c_p,
+                          _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p], ctypes.c_int),
+    "rfp2_moe_route": ([_c_p, _c_i64, _c_i64, _c_i64, _c_p, ctypes.c_int, _c_i64, _c_i64, _c_i64,
+                        _c_i64, ctypes.c_int, _c_f64, _c_p, _c_p, _c_p, _c_p], ctypes.c_int),
+    "rfp2_quantize_gated_acts": ([_c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int, _c_p,
+                                  _c_p, _c_p], ctypes.c_int),
+    "rfp2_dequantize_acts": ([_c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p], ctypes.c_int),
     "rfp2_read_ceiling": ([_c_p, _c_i64, ctypes.c_uint32, _c_p, _c_p], ctypes.c_int),
     "rfp2_quant_gemv": ([_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p], ctypes.c_int),
     "rfp2_quant_moe_gemv": ([_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p,
@@ -511,6 +524,104 @@ def rfp2_paged_attn(cache, q, B: int, new_tokens: int, H: int, lens, scale: floa
         ref, qp, B, new_tokens, H, qs, _ptr(lens, torch.int32, B, "lens"), scale,
         window, _ptr(y, torch.float32, rows * width, "y"), errp,
         _ptr(workspace, torch.uint8, 0, "workspace"), workspace.numel(), _stream(stream)))
+
+
+def _here(*tensors):
+    """Every tensor that is there on the GPU whose stream the call goes to."""
+    import torch
+    gpu = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != gpu:
+            raise ValueError(f"a tensor of the call is on {t.device}, the current GPU is cuda:{gpu}")
+
+
+def rfp2_rms_norm(x, T: int, H: int, D: int, gain, eps: float, y, stream=None) -> None:
+    """x, y: T rows of H * D values ([T, H, D] or [T, H * D]); rows may lie
+    apart.  y may be x."""
+    import torch
+    xp, xs = _rows(x, T, H * D, "x")
+    yp, ys = _rows(y, T, H * D, "y")
+    gp = _ptr(gain, torch.float32, D, "gain")
+    _here(x, y, gain)
+    _check("rfp2_rms_norm", lib().rfp2_rms_norm(xp, T, H, D, xs, gp, eps, yp, ys,
+                                                _stream(stream)))
+
+
+def _norm_out(T: int, K: int, h, y, q, d):
+    """Pointers and strides of what a norm of rows writes (None: not wanted)."""
+    import torch
+    hp, hs = (None, 0) if h is None else _rows(h, T, K, "h")
+    yp, ys = (None, 0) if y is None else _rows(y, T, K, "y")
+    qp = None if q is None else _ptr(q, torch.int8, T * K, "q")
+    dp = None if d is None else _ptr(d, torch.float32, T * _blocks(K), "d")
+    return hp, hs, yp, ys, qp, dp
+
+
+def rfp2_add_rms_norm(x, add, T: int, K: int, gain, eps: float, h=None, y=None, q=None, d=None,
+                      stream=None) -> None:
+    """x, add, h, y: T rows of K values; rows may lie apart.  add and h, y, or q
+    and d may be None; h and y may each be x or add."""
+    import torch
+    xp, xs = _rows(x, T, K, "x")
+    ap, as_ = (None, 0) if add is None else _rows(add, T, K, "add")
+    gp = _ptr(gain, torch.float32, K, "gain")
+    hp, hs, yp, ys, qp, dp = _norm_out(T, K, h, y, q, d)
+    _here(x, add, gain, h, y, q, d)
+    _check("rfp2_add_rms_norm", lib().rfp2_add_rms_norm(
+        xp, ap, T, K, xs, as_, gp, eps, hp, hs, yp, ys, qp, dp, _stream(stream)))
+
+
+def rfp2_moe_combine(x, rows, weights, T: int, top_k: int, K: int, h=None, gain=None,
+                     eps: float = 0.0, y=None, q=None, d=None, stream=None) -> None:
+    """x, h, y: T rows of K values; rows may lie apart.  rows: [T, top_k, K],
+    weights: [T, top_k], contiguous.  x may be None; without a gain only h is
+    written."""
+    import torch
+    xp, xs = (None, 0) if x is None else _rows(x, T, K, "x")
+    rp = _ptr(rows, torch.float32, T * top_k * K, "rows")
+    wp = _ptr(weights, torch.float32, T * top_k, "weights")
+    gp = None if gain is None else _ptr(gain, torch.float32, K, "gain")
+    hp, hs, yp, ys, qp, dp = _norm_out(T, K, h, y, q, d)
+    _here(x, rows, weights, gain, h, y, q, d)
+    _check("rfp2_moe_combine", lib().rfp2_moe_combine(
+        xp, rp, wp, T, top_k, K, xs, gp, eps, hp, hs, yp, ys, qp, dp, _stream(stream)))
+
+
+def rfp2_moe_route(logits, T: int, E: int, bias, score: int, groups: int, group_top: int,
+                   top_groups: int, top_k: int, renorm: bool, scale: float, ids, weights,
+                   err=None, stream=None) -> None:
+    """logits: T rows of E values; rows may lie apart.  bias may be None."""
+    import torch
+    lp, ls = _rows(logits, T, E, "logits")
+    bp = None if bias is None else _ptr(bias, torch.float32, E, "bias")
+    ip = _ptr(ids, torch.int32, T * top_k, "ids")
+    wp = _ptr(weights, torch.float32, T * top_k, "weights")
+    errp = None if err is None else _ptr(err, torch.int32, 1, "err")
+    _here(logits, bias, ids, weights, err)
+    _check("rfp2_moe_route", lib().rfp2_moe_route(
+        lp, T, E, ls, bp, score, groups, group_top, top_groups, top_k, bool(renorm), scale, ip, wp,
+        errp, _stream(stream)))
+
+
+def rfp2_quantize_gated_acts(gate, up, M: int, K: int, act: int, q, d, stream=None) -> None:
+    """gate, up: M rows of K values; rows may lie apart (two halves of one product)."""
+    import torch
+    gp, gs = _rows(gate, M, K, "gate")
+    up_, us = _rows(up, M, K, "up")
+    qp = _ptr(q, torch.int8, M * K, "q")
+    dp = _ptr(d, torch.float32, M * _blocks(K), "d")
+    _here(gate, up, q, d)
+    _check("rfp2_quantize_gated_acts", lib().rfp2_quantize_gated_acts(
+        gp, up_, M, K, gs, us, act, qp, dp, _stream(stream)))
+
+
+def rfp2_dequantize_acts(q, d, M: int, K: int, a, stream=None) -> None:
+    import torch
+    qp = _ptr(q, torch.int8, M * K, "q")
+    dp = _ptr(d, torch.float32, M * _blocks(K), "d")
+    ap = _ptr(a, torch.float32, M * K, "a")
+    _here(q, d, a)
+    _check("rfp2_dequantize_acts", lib().rfp2_dequantize_acts(qp, dp, M, K, ap, _stream(stream)))
 
 
 def rfp2_debug_decode(w, N: int, K: int, codes_out, scales_out, stream=None) -> None:

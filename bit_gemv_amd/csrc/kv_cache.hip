@@ -76,40 +76,11 @@ __device__ __forceinline__ int64_t first_token(const int32_t* pos, int64_t block
   return TG == 1 ? block : block * TG - (pos[0] & 7);
 }
 
-// Code and scale as quantize_acts_kernel computes them, of four of the eight lanes' 32
-// values.  Magnitudes are compared as integers, where infinities and NaN are the largest.
-__device__ __forceinline__ float quantize4(const float (&x)[4], uint32_t& codes) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  // over the eight lanes: neighbours, pairs, then the other four in reverse
-  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true));
-  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, true));
-  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x141, 0xF, 0xF, true));
-  const bool finite = top < 0x7F800000u;
-  const float scale =
-      finite ? __fdiv_rn(__uint_as_float(top), 127.0f) : __builtin_nanf("");
-  codes = 0;
-  if (finite && scale != 0.0f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float r = fminf(fmaxf(roundf(__fdiv_rn(x[i], scale)), -127.0f), 127.0f);
-      codes |= ((uint32_t)(int32_t)r & 0xFFu) << (8 * i);
-    }
-  }
-  return scale;
-}
-
 __device__ __forceinline__ uint2 halves4(const float (&x)[4]) {
   union { __half h[4]; uint2 u; } o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o.h[i] = __float2half_rn(x[i]);
   return o.u;
-}
-
-__device__ __forceinline__ void load4(float (&x)[4], const float* p) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
 
 // The four values x from d on of a head at `src`, turned.

@@ -75,6 +75,24 @@ rfp2_status check_kv_rows(const rfp2::KvView& c, const void* k, const void* v, i
   return RFP2_OK;
 }
 
+// The norm of rows: what rfp2_add_rms_norm and rfp2_moe_combine share.
+rfp2_status check_norm(const float* x, int64_t T, int64_t K, int64_t x_stride, const float* gain,
+                       double eps, const float* h, int64_t h_stride, const float* y,
+                       int64_t y_stride, const int8_t* q, const float* d) {
+  if (!gain ? (!h || y || q || d) : (!y && !q)) return RFP2_E_NULL;
+  if (!q != !d) return RFP2_E_NULL;
+  if (T < 1 || T > kMaxRows || K < 4 || K > (int64_t(1) << 24) || K % (q ? 32 : 4) != 0 ||
+      (x && !row_stride_ok(x_stride, K)) || (h && !row_stride_ok(h_stride, K)) ||
+      (y && !row_stride_ok(y_stride, K)) || (gain && (!std::isfinite(eps) || !(eps > 0.0))) ||
+      (h && h == y) || (h && h == x && h_stride != x_stride) ||
+      (y && y == x && y_stride != x_stride))
+    return RFP2_E_SHAPE;
+  if (!aligned(x, 16) || !aligned(gain, 16) || !aligned(h, 16) || !aligned(y, 16) ||
+      !aligned(q, 4) || !aligned(d, 4))
+    return RFP2_E_ALIGN;
+  return RFP2_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -364,6 +382,100 @@ rfp2_status rfp2_paged_attn(const rfp2_kv_cache* cache, const float* q, int64_t 
   return from_hip(rfp2::launch_paged_attn(c, cache->format == RFP2_KV_I8, q, B, new_tokens, H,
                                           q_stride, lens, scale, window, y, err, workspace,
                                           stream));
+}
+
+rfp2_status rfp2_rms_norm(const float* x, int64_t T, int64_t H, int64_t D, int64_t x_stride,
+                          const float* gain, double eps, float* y, int64_t y_stride,
+                          hipStream_t stream) {
+  if (!x || !gain || !y) return RFP2_E_NULL;
+  if (T < 1 || T > kMaxRows || H < 1 || D < 4 || D > rfp2::kMaxRopeDim || D % 4 != 0 ||
+      H > (int64_t(1) << 24) / D || !row_stride_ok(x_stride, H * D) ||
+      !row_stride_ok(y_stride, H * D) || (x == y && x_stride != y_stride) ||
+      !std::isfinite(eps) || !(eps > 0.0))
+    return RFP2_E_SHAPE;
+  if (!aligned(x, 16) || !aligned(gain, 16) || !aligned(y, 16)) return RFP2_E_ALIGN;
+  (void)hipGetLastError();
+  return from_hip(rfp2::launch_rms_norm(x, T, H, D, x_stride, gain, eps, y, y_stride, stream));
+}
+
+rfp2_status rfp2_add_rms_norm(const float* x, const float* add, int64_t T, int64_t K,
+                              int64_t x_stride, int64_t add_stride, const float* gain, double eps,
+                              float* h, int64_t h_stride, float* y, int64_t y_stride, int8_t* q,
+                              float* d, hipStream_t stream) {
+  if (!x || !gain) return RFP2_E_NULL;
+  const rfp2_status st =
+      check_norm(x, T, K, x_stride, gain, eps, h, h_stride, y, y_stride, q, d);
+  if (st != RFP2_OK) return st;
+  if (h && !add) return RFP2_E_SHAPE;
+  if (add && (!row_stride_ok(add_stride, K) || (h == add && h_stride != add_stride) ||
+              (y == add && y_stride != add_stride)))
+    return RFP2_E_SHAPE;
+  if (!aligned(add, 16)) return RFP2_E_ALIGN;
+  (void)hipGetLastError();
+  return from_hip(rfp2::launch_add_rms_norm(x, add, T, K, x_stride, add_stride, gain, eps, h,
+                                            h_stride, y, y_stride, q, d, stream));
+}
+
+rfp2_status rfp2_moe_combine(const float* x, const float* rows, const float* weights, int64_t T,
+                             int64_t top_k, int64_t K, int64_t x_stride, const float* gain,
+                             double eps, float* h, int64_t h_stride, float* y, int64_t y_stride,
+                             int8_t* q, float* d, hipStream_t stream) {
+  if (!rows || !weights) return RFP2_E_NULL;
+  const rfp2_status st =
+      check_norm(x, T, K, x_stride, gain, eps, h, h_stride, y, y_stride, q, d);
+  if (st != RFP2_OK) return st;
+  if (top_k < 1 || top_k > 1024 || T > kMaxRows / top_k || h == rows || y == rows)
+    return RFP2_E_SHAPE;
+  if (!aligned(rows, 16) || !aligned(weights, 4)) return RFP2_E_ALIGN;
+  (void)hipGetLastError();
+  return from_hip(rfp2::launch_moe_combine(x, rows, weights, T, top_k, K, x_stride, gain, eps, h,
+                                           h_stride, y, y_stride, q, d, stream));
+}
+
+rfp2_status rfp2_moe_route(const float* logits, int64_t T, int64_t E, int64_t stride,
+                           const float* bias, int score, int64_t groups, int64_t group_top,
+                           int64_t top_groups, int64_t top_k, int renorm, double scale,
+                           int32_t* ids, float* weights, int32_t* err, hipStream_t stream) {
+  if (!logits || !ids || !weights || (group_top == 2 && !bias)) return RFP2_E_NULL;
+  if (T < 1 || T > kMaxRows || E < 1 || E > rfp2::kMaxSortExperts || stride < E ||
+      stride > (int64_t(1) << 40) ||
+      (score != RFP2_ROUTE_SOFTMAX && score != RFP2_ROUTE_SIGMOID) || groups < 1 || groups > 64 ||
+      E % groups != 0 || top_groups < 1 || top_groups > groups || top_k < 1 || top_k > 64 ||
+      top_k > top_groups * (E / groups) || group_top < 1 || group_top > 2 ||
+      group_top > E / groups || !std::isfinite(scale))
+    return RFP2_E_SHAPE;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(err, 4))
+    return RFP2_E_ALIGN;
+  (void)hipGetLastError();
+  return from_hip(rfp2::launch_moe_route(logits, T, E, stride, bias, score == RFP2_ROUTE_SIGMOID,
+                                         (int)groups, (int)group_top, (int)top_groups, (int)top_k,
+                                         renorm != 0, scale, ids, weights, err, stream));
+}
+
+rfp2_status rfp2_quantize_gated_acts(const float* gate, const float* up, int64_t M, int64_t K,
+                                     int64_t gate_stride, int64_t up_stride, int act, int8_t* q,
+                                     float* d, hipStream_t stream) {
+  if (!gate || !up || !q || !d) return RFP2_E_NULL;
+  if (M < 1 || M > kMaxRows || K < 32 || K % 32 != 0 || K > (int64_t(1) << 24) ||
+      !row_stride_ok(gate_stride, K) || !row_stride_ok(up_stride, K) ||
+      (act != RFP2_GATE_SILU && act != RFP2_GATE_GELU))
+    return RFP2_E_SHAPE;
+  if (!aligned(gate, 16) || !aligned(up, 16) || !aligned(q, 4) || !aligned(d, 4))
+    return RFP2_E_ALIGN;
+  (void)hipGetLastError();
+  return from_hip(rfp2::launch_quantize_gated_acts(gate, up, M, K, gate_stride, up_stride,
+                                                   act == RFP2_GATE_GELU, q, d, stream));
+}
+
+rfp2_status rfp2_dequantize_acts(const int8_t* q, const float* d, int64_t M, int64_t K, float* a,
+                                 hipStream_t stream) {
+  if (!q || !d || !a) return RFP2_E_NULL;
+  if (M < 1 || M > kMaxRows || K < 32 || K % 32 != 0 || K > (int64_t(1) << 30))
+    return RFP2_E_SHAPE;
+  if (!aligned(q, 4) || !aligned(d, 4) || !aligned(a, 16)) return RFP2_E_ALIGN;
+  (void)hipGetLastError();
+  return from_hip(rfp2::launch_dequantize_acts(q, d, M, K, a, stream));
 }
 
 rfp2_status rfp2_read_ceiling(const uint8_t* buf, int64_t bytes, uint32_t magic, uint32_t* out,

@@ -99,6 +99,26 @@ hipError_t launch_paged_attn(const KvView& c, bool i8, const float* q, int64_t B
                              int64_t new_tokens, int64_t H, int64_t q_stride,
                              const int32_t* lens, float scale, int64_t window, float* y,
                              int32_t* err, void* workspace, hipStream_t stream);
+hipError_t launch_rms_norm(const float* x, int64_t T, int64_t H, int64_t D, int64_t x_stride,
+                           const float* gain, double eps, float* y, int64_t y_stride,
+                           hipStream_t stream);
+hipError_t launch_add_rms_norm(const float* x, const float* add, int64_t T, int64_t K,
+                               int64_t x_stride, int64_t add_stride, const float* gain,
+                               double eps, float* h, int64_t h_stride, float* y,
+                               int64_t y_stride, int8_t* q, float* d, hipStream_t stream);
+hipError_t launch_moe_combine(const float* x, const float* rows, const float* weights, int64_t T,
+                              int64_t top_k, int64_t K, int64_t x_stride, const float* gain,
+                              double eps, float* h, int64_t h_stride, float* y,
+                              int64_t y_stride, int8_t* q, float* d, hipStream_t stream);
+hipError_t launch_moe_route(const float* logits, int64_t T, int64_t E, int64_t stride,
+                            const float* bias, bool sigmoid, int groups, int group_top,
+                            int top_groups, int top_k, bool renorm, double scale, int32_t* ids,
+                            float* weights, int32_t* err, hipStream_t stream);
+hipError_t launch_quantize_gated_acts(const float* gate, const float* up, int64_t M, int64_t K,
+                                      int64_t gate_stride, int64_t up_stride, bool gelu,
+                                      int8_t* q, float* d, hipStream_t stream);
+hipError_t launch_dequantize_acts(const int8_t* q, const float* d, int64_t M, int64_t K, float* a,
+                                  hipStream_t stream);
 hipError_t launch_read_ceiling(const uint8_t* buf, int64_t bytes, uint32_t magic, uint32_t* out,
                                hipStream_t stream);
 hipError_t launch_debug_decode(const uint8_t* w, int64_t N, int64_t K,

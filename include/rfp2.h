@@ -484,6 +484,138 @@ rfp2_status rfp2_paged_attn(const rfp2_kv_cache* cache, const float* q, int64_t 
                             hipStream_t stream);
 
 /*
+ * The calls around the products of a feed-forward part, dense or routed: the
+ * norm that adds to the residual stream and quantizes, the routing of tokens
+ * to experts, the gate's activation between two products, and the experts'
+ * weighted sum back onto the stream.  fp32 rows come in; what a product takes
+ * next goes out (int8 activations exactly as rfp2_quantize_acts gives them
+ * for the fp32 values, expert ids).  Inner arithmetic is fp64 with one
+ * rounding to fp32, so that codes and choices are those of the definition;
+ * infinities and NaN go through the formulas (a block of 32 that holds one
+ * gets d = NaN, q = 0).
+ *
+ * rfp2_rms_norm -- the norm of each head (of a query or key before rfp2_rope):
+ *   y = x * gain / sqrt(mean over the head of x^2 + eps).
+ *   x, y  T rows of H heads of D values, row t at x + t * x_stride and
+ *         y + t * y_stride; 16-byte aligned.  y == x with equal strides works
+ *         in place; any other overlap is not allowed.
+ *   gain  [D], the same for all heads; 16-byte aligned.
+ * Requires T >= 1, H >= 1, 4 <= D <= 1024, D % 4 == 0, H * D <= 2^24, strides
+ * >= H * D and multiples of 4, eps > 0 and finite.
+ */
+rfp2_status rfp2_rms_norm(const float* x, int64_t T, int64_t H, int64_t D, int64_t x_stride,
+                          const float* gain, double eps, float* y, int64_t y_stride,
+                          hipStream_t stream);
+
+/*
+ * rfp2_add_rms_norm -- a product's rows added to the residual stream, and the
+ * norm of the sum as the next product's input:
+ *   h = x + add,  y = h * gain / sqrt(mean over the row of h^2 + eps),
+ *   q, d = rfp2_quantize_acts of y.
+ *   x, add, h, y  T rows of K values, row t at x + t * x_stride and so on;
+ *         16-byte aligned.  add may be NULL (h is then NULL too: the norm of
+ *         x); h, y, and q with d may be NULL where they are not wanted, but
+ *         not y and q both.  h and y may each be x or add with equal strides
+ *         (not both the same one); any other overlap is not allowed.
+ *   gain  [K], 16-byte aligned.
+ *   q [T][K] int8, d [T][K/32] fp32, both 4-byte aligned (16 for q where a
+ *         product reads it).
+ * Requires T >= 1, 4 <= K <= 2^24, K % 4 == 0 (K % 32 == 0 with q), strides
+ * (of what is there) >= K and multiples of 4, eps > 0 and finite.
+ */
+rfp2_status rfp2_add_rms_norm(const float* x, const float* add, int64_t T, int64_t K,
+                              int64_t x_stride, int64_t add_stride, const float* gain, double eps,
+                              float* h, int64_t h_stride, float* y, int64_t y_stride, int8_t* q,
+                              float* d, hipStream_t stream);
+
+/*
+ * rfp2_moe_combine -- the routed experts' rows summed by their weights onto the
+ * residual stream, with the norm that follows (rfp2_add_rms_norm's) in the same
+ * pass:
+ *   h = x + sum_j weights[t][j] * rows[t][j]   (fp64, rounded once).
+ *   x, h, y, gain, q, d  as rfp2_add_rms_norm; x may be NULL (nothing is added
+ *         to).  With gain NULL there is no norm (eps is not read), y, q and d are
+ *         NULL and h is not; with a gain, h may be NULL but not y and q both.
+ *         h and y may each be x with equal strides (not both).
+ *   rows     [T][top_k][K] fp32, 16-byte aligned: what rfp2_moe_gemv,
+ *         rfp2_moe_gemv_tokens and rfp2_moe_gemm write.
+ *   weights  [T][top_k] fp32, 4-byte aligned.
+ * A weight of 0 does not take out a row that holds NaN or infinity.
+ * Requires 1 <= top_k <= 1024, T * top_k <= 2^30, the limits of
+ * rfp2_add_rms_norm otherwise.
+ */
+rfp2_status rfp2_moe_combine(const float* x, const float* rows, const float* weights, int64_t T,
+                             int64_t top_k, int64_t K, int64_t x_stride, const float* gain,
+                             double eps, float* h, int64_t h_stride, float* y, int64_t y_stride,
+                             int8_t* q, float* d, hipStream_t stream);
+
+/* How a router's logits become scores. */
+#define RFP2_ROUTE_SOFTMAX 0 /* p = exp(l) / sum over the experts of exp(l) */
+#define RFP2_ROUTE_SIGMOID 1 /* p = 1 / (1 + exp(-l))                       */
+
+/*
+ * rfp2_moe_route -- the experts of each token and their weights, from the
+ * router's logits: the ids that rfp2_moe_gemv and its kin take, the weights
+ * that rfp2_moe_combine takes.
+ *   logits [T] rows of E fp32, row t at logits + t * stride; 4-byte aligned.
+ *   bias   nullable [E] fp32, 4-byte aligned: added to the scores for the
+ *          choice only (a balance among the experts); finite.
+ *   v_e = p_e + bias_e, or v_e = logits_e without a bias.  With groups > 1 the
+ *   experts form `groups` runs of E / groups; a group counts by the sum of its
+ *   group_top (1 or 2) largest v (by those that are not masked), and only the
+ *   top_groups best groups stay.  The top_k largest v among what stays are
+ *   chosen, in falling order; among equal groups or experts the lower comes
+ *   first.  v and p are fp64.
+ *   ids     [T][top_k] int32, 4-byte aligned.
+ *   weights [T][top_k] fp32, 4-byte aligned: scale * p of the chosen, where
+ *          renorm != 0 divided by the sum of the chosen p (0 where that is 0).
+ *   err     nullable device int32: a token with a logit of NaN or plus infinity,
+ *          or any bias that is not finite, gets ids of -1 and weights of NaN, and
+ *          1 is written to *err (never cleared by the call).
+ * A logit of minus infinity masks its expert: p = 0, and it is chosen only where
+ * fewer than top_k others stay (with weight 0; the lower first).  A token whose
+ * logits are all minus infinity gets valid ids and weights of 0.
+ * Requires T >= 1, 1 <= E <= 2048, stride >= E, 1 <= top_k <= 64, groups from 1 to
+ * 64 dividing E, 1 <= top_groups <= groups, top_k <= top_groups * (E / groups),
+ * group_top 1, or 2 with a bias and E / groups >= 2, scale finite.
+ */
+rfp2_status rfp2_moe_route(const float* logits, int64_t T, int64_t E, int64_t stride,
+                           const float* bias, int score, int64_t groups, int64_t group_top,
+                           int64_t top_groups, int64_t top_k, int renorm, double scale,
+                           int32_t* ids, float* weights, int32_t* err, hipStream_t stream);
+
+/* The activation of a gate. */
+#define RFP2_GATE_SILU 0 /* g / (1 + exp(-g))                                            */
+#define RFP2_GATE_GELU 1 /* 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))            */
+
+/*
+ * rfp2_quantize_gated_acts -- act(gate) * up as int8 activations: what lies
+ * between the gate and up products and the down product of a feed-forward part.
+ *   gate, up  M rows of K fp32, row m at gate + m * gate_stride and up + m *
+ *             up_stride (two halves of one product's rows, or two products);
+ *             16-byte aligned.
+ *   act       one of the two above.
+ *   q [M][K] int8, d [M][K/32] fp32: rfp2_quantize_acts of the product's fp32
+ *             values; 4-byte aligned, no overlap with gate or up.
+ * Requires M >= 1, K >= 32, K % 32 == 0, K <= 2^24, strides >= K and multiples
+ * of 4.
+ */
+rfp2_status rfp2_quantize_gated_acts(const float* gate, const float* up, int64_t M, int64_t K,
+                                     int64_t gate_stride, int64_t up_stride, int act, int8_t* q,
+                                     float* d, hipStream_t stream);
+
+/*
+ * rfp2_dequantize_acts -- the values that int8 activations stand for,
+ * a = fl32(q * d): the reverse of rfp2_quantize_acts (a router or any other
+ * reader of fp32 values can follow a call that wrote q and d alone).
+ *   q, d as rfp2_quantize_acts writes them, 4-byte aligned; a [M][K] fp32,
+ *   16-byte aligned.
+ * Requires M >= 1, K >= 32, K % 32 == 0, K <= 2^30.
+ */
+rfp2_status rfp2_dequantize_acts(const int8_t* q, const float* d, int64_t M, int64_t K, float* a,
+                                 hipStream_t stream);
+
+/*
  * rfp2_read_ceiling -- measurement helper, not part of the method: reads
  * `bytes` bytes of buf once with the plainest coalesced 16-byte loads
  * (thread t of the grid reads pieces t, t + T, t + 2T, ... of 16 bytes,

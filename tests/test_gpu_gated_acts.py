@@ -1,0 +1,101 @@
+"""GPU parity of the quantized gate activation and of the values that int8 activations
+stand for, against the fp64 oracle."""
+import numpy as np
+import pytest
+
+import bit_gemv_amd as rf
+import oracle
+from _gpu import announce, device, empty, host, to_dev, torch
+from _layer import assert_codes
+from oracle import feed_forward as ff
+
+pytestmark = pytest.mark.gpu
+
+SIZES = [(1, 32), (8, 1536), (3, 96), (33, 2048), (7, 4128), (1, 14336), (1100, 64), (600, 1536), (2, 65536),
+         (5, 160)]
+
+
+def run(g, u, act, M, K):
+    q = torch.full((M + 1, K), 99, dtype=torch.int8, device=device())
+    d = torch.full((M + 1, K // 32), -7.0, device=device())
+    rf.rfp2_quantize_gated_acts(g, u, M, K, act, q, d)
+    assert (host(q)[M] == 99).all() and (host(d)[M] == -7.0).all()
+    return host(q)[:M], host(d)[:M]
+
+
+@pytest.mark.parametrize("M,K", SIZES)
+@pytest.mark.parametrize("act", [rf.GATE_SILU, rf.GATE_GELU])
+def test_gate(M, K, act):
+    announce("quantize_gated_acts", M, K, act)
+    rng = np.random.default_rng(M + K)
+    gu = (2.0 * rng.standard_normal((M, 2 * K))).astype(np.float32)
+    ref = ff.gated(gu[:, :K], gu[:, K:], act == rf.GATE_GELU)
+    both = to_dev(gu)
+    q, d = run(both[:, :K], both[:, K:], act, M, K)               # two halves of one product
+    assert_codes(q, d, ref)
+    # codes and scales are those of the quantizer on the rounded values, but for values whose
+    # rounding to fp32 hangs on the last bits of the fp64 arithmetic
+    q2, d2 = oracle.quantize_acts(ref.astype(np.float32))
+    assert np.array_equal(q, q2) and np.array_equal(d, d2)
+    g2, u2 = both[:, :K].contiguous(), both[:, K:].contiguous()   # two products
+    q3, d3 = run(g2, u2, act, M, K)
+    assert np.array_equal(q, q3) and np.array_equal(d, d3)
+
+
+@pytest.mark.parametrize("act", [rf.GATE_SILU, rf.GATE_GELU])
+def test_range_of_the_gate(act):
+    """From gates that vanish to gates that pass, with other halves that bring them back into
+    range: silu(-100) is 4e-42 in fp32 and has three bits there; times 1e38 it has all of them."""
+    announce("gate range", act)
+    g = np.concatenate([np.linspace(-120, 120, 1024), -np.logspace(-30, 2, 512), np.logspace(-30, 20, 512),
+                        -np.logspace(2, 30, 128)]).astype(np.float32)
+    g = np.concatenate([g, np.zeros(-len(g) % 32, dtype=np.float32)])
+    K = len(g)
+    for size in (1.0, 1e-20, 1e18):
+        u = np.full(K, size, dtype=np.float32)
+        with np.errstate(over="ignore"):
+            ref = ff.gated(g, u, act == rf.GATE_GELU)
+        keep = np.abs(ref) < 1e38                                 # beyond: infinity in fp32, a NaN block
+        u[~keep], ref[~keep] = 0.0, 0.0
+        q, d = run(to_dev(g[None]), to_dev(u[None]), act, 1, K)
+        assert_codes(q, d, ref[None])
+
+
+@pytest.mark.parametrize("act", [rf.GATE_SILU, rf.GATE_GELU])
+def test_infinities_and_nan(act):
+    announce("gate of infinities", act)
+    rng = np.random.default_rng(2)
+    M, K = 5, 128
+    g, u = rng.standard_normal((2, M, K)).astype(np.float32)
+    g[0, 3], g[1, 40], g[2, 70], u[3, 127], u[4, 0] = np.nan, np.inf, -np.inf, np.nan, -np.inf
+    q, d = run(to_dev(g), to_dev(u), act, M, K)
+    ref = ff.gated(g, u, act == rf.GATE_GELU)
+    for m, b in ((0, 0), (1, 1), (2, 2), (3, 3), (4, 0)):
+        assert np.isnan(d[m, b]) and not q[m, 32 * b:32 * b + 32].any()
+        rest = [i for i in range(4) if i != b]
+        r = ref[m].reshape(4, 32)[rest].reshape(1, -1)
+        assert_codes(q[m].reshape(4, 32)[rest].reshape(1, -1), d[m, rest][None], r)
+
+
+@pytest.mark.parametrize("M,K", [(1, 32), (3, 96), (7, 5120), (1030, 4096), (1, 1 << 20)])
+def test_values_of_codes(M, K):
+    announce("dequantize_acts", M, K)
+    rng = np.random.default_rng(M)
+    a = (rng.standard_normal((M, K)) * np.exp(4 * rng.standard_normal((M, 1)))).astype(np.float32)
+    q, d = empty((M, K), torch.int8), empty((M, K // 32), torch.float32)
+    rf.rfp2_quantize_acts(to_dev(a), M, K, q, d)
+    out = torch.full((M + 1, K), -7.0, device=device())
+    rf.rfp2_dequantize_acts(q, d, M, K, out)
+    want = host(q).reshape(M, K // 32, 32).astype(np.float32) * host(d)[..., None]
+    assert np.array_equal(host(out)[:M], want.reshape(M, K)) and (host(out)[M] == -7.0).all()
+
+
+def test_values_of_all_codes():
+    announce("dequantize_acts, all codes")
+    q = np.arange(-128, 128, dtype=np.int8).reshape(2, 128)
+    d = np.array([[1.0, 2.0 ** -149, np.nan, -3.5], [0.0, np.inf, 1e30, 0.1]], dtype=np.float32)
+    out = empty((2, 128), torch.float32)
+    rf.rfp2_dequantize_acts(to_dev(q), to_dev(d), 2, 128, out)
+    with np.errstate(invalid="ignore"):
+        want = (q.reshape(2, 4, 32).astype(np.float32) * d[..., None]).reshape(2, 128)
+    assert np.array_equal(host(out), want, equal_nan=True)
