@@ -16,28 +16,44 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The sum over the wave, in every lane.
-__device__ __forceinline__ double wave_sum(double s) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
-  return s;
-}
-
-// One wave a head of D values: heads [.., 4 * blockIdx.y + wave, ..] of row blockIdx.x.
+// Norm of heads: G lanes own a head of D values, C times four each; a workgroup takes 256 / G
+// heads of row blockIdx.x.
+template <int G, int C, bool NT>
 __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const float* x, int H, int D,
                                                             int64_t x_stride,
                                                             const float* __restrict__ gain,
                                                             double eps, float* y,
                                                             int64_t y_stride) {
-  const int lane = threadIdx.x & 63;
-  const int h = blockIdx.y * (kThreads / 64) + (threadIdx.x >> 6);
-  if (h >= H) return;
+  const int lane = threadIdx.x & (G - 1);
+  const int h = blockIdx.y * (kThreads / G) + threadIdx.x / G;
+  if (h >= H) return;                        // all of a head's lanes
   const float* xr = x + blockIdx.x * x_stride + (int64_t)h * D;
   float* yr = y + blockIdx.x * y_stride + (int64_t)h * D;
+  float v[C][4], g[C][4];
   double s = 0.0;
-  for (int i = lane; i < D; i += 64) s += (double)xr[i] * xr[i];
-  const double inv = 1.0 / sqrt(wave_sum(s) / D + eps);
-  for (int i = lane; i < D; i += 64) yr[i] = (float)((double)xr[i] * inv * gain[i]);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = 4 * (lane + c * G);
+    if (i < D) {
+      load4(v[c], xr + i);
+      load4(g[c], gain + i);
+    } else {
+      v[c][0] = v[c][1] = v[c][2] = v[c][3] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s = fma((double)v[c][e], (double)v[c][e], s);
+  const double inv = 1.0 / sqrt(group_sum<G>(s) / D + eps);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = 4 * (lane + c * G);
+    if (i >= D) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[c][e] = (float)((double)v[c][e] * inv * (double)g[c][e]);
+    store4<NT>(yr + i, make_float4(v[c][0], v[c][1], v[c][2], v[c][3]));
+  }
 }
 
 // Where a row comes from and goes to; what is null is not there.
@@ -55,77 +71,186 @@ struct NormRows {
   int32_t top_k;
 };
 enum { MODE_ROW, MODE_ADD, MODE_SUM };
+// What goes past the caches: nothing, what is written in fp32, the rows that are read too.
+enum { KEEP, STREAM_OUT, STREAM_ALL };
 
 // Values 4 * i .. 4 * i + 3 of row t of the stream.
-template <int MODE>
+template <int MODE, bool NT>
 __device__ __forceinline__ void stream4(float (&v)[4], const NormRows& r, int64_t t, int64_t i) {
-  if (r.x) load4(v, r.x + t * r.x_stride + 4 * i);
+  if (MODE != MODE_SUM || r.x) load4<NT>(v, r.x + t * r.x_stride + 4 * i);
   else v[0] = v[1] = v[2] = v[3] = 0.0f;
   if constexpr (MODE == MODE_ADD) {
     float a[4];
-    load4(a, r.add + t * r.add_stride + 4 * i);
+    load4<NT>(a, r.add + t * r.add_stride + 4 * i);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] += a[e];
   }
   if constexpr (MODE == MODE_SUM) {
     double s[4] = {v[0], v[1], v[2], v[3]};
+    const float* w = r.weights + t * r.top_k;
+    const float* a0 = r.add + t * r.top_k * r.K + 4 * i;
+#pragma unroll 8
     for (int j = 0; j < r.top_k; ++j) {
       float a[4];
-      const double w = r.weights[t * r.top_k + j];
-      load4(a, r.add + (t * r.top_k + j) * r.K + 4 * i);
+      load4(a, a0 + j * r.K);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = fma(w, (double)a[e], s[e]);
+      for (int e = 0; e < 4; ++e) s[e] = fma((double)w[j], (double)a[e], s[e]);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = (float)s[e];
   }
 }
 
-// One workgroup a row.  A thread reads back only what it wrote itself, so h and y may
-// be the rows that were read.
-template <int MODE>
-__global__ __launch_bounds__(kThreads) void row_norm_kernel(NormRows r, int64_t row0) {
-  __shared__ double part[kThreads / 64];
+template <bool NT>
+__device__ __forceinline__ void put_normed(float (&v)[4], const float (&g)[4], double inv,
+                                           const NormRows& r, int64_t t, int64_t i) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (float)((double)v[e] * inv * (double)g[e]);
+  if (r.y) store4<NT>(r.y + t * r.y_stride + 4 * i, make_float4(v[0], v[1], v[2], v[3]));
+  if (r.q) {
+    const int64_t at = t * (r.K >> 2) + i;
+    uint32_t codes;
+    const float scale = quantize4(v, codes);
+    r.q[at] = codes;
+    if ((threadIdx.x & 7) == 0) r.d[at >> 3] = scale;
+  }
+}
+
+// One workgroup a row; C quads of a thread stay in registers, what a row has beyond is
+// read again.  A thread reads back only what it wrote itself, so h and y may be the rows
+// that were read.
+template <int MODE, int THREADS, int C, int PAST>
+__global__ __launch_bounds__(THREADS) void row_norm_kernel(NormRows r, int64_t row0) {
+  __shared__ double part[THREADS / 64];
   const int64_t t = row0 + blockIdx.x, quads = r.K >> 2;
+  float v[C][4], g[C][4];
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < quads; i += kThreads) {
-    float v[4];
-    stream4<MODE>(v, r, t, i);
-    if (r.h) store4<false>(r.h + t * r.h_stride + 4 * i, make_float4(v[0], v[1], v[2], v[3]));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s = fma((double)v[e], (double)v[e], s);
+  for (int c = 0; c < C; ++c) {
+    const int64_t i = threadIdx.x + c * THREADS;
+    if (i < quads) stream4<MODE, PAST == STREAM_ALL>(v[c], r, t, i);
+    else v[c][0] = v[c][1] = v[c][2] = v[c][3] = 0.0f;
   }
-  if (!r.gain) return;
-  s = wave_sum(s);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
-  __syncthreads();
-  s = 0.0;
-  for (int w = 0; w < kThreads / 64; ++w) s += part[w];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int64_t i = threadIdx.x + c * THREADS;
+    if (i < quads) load4(g[c], r.gain + 4 * i);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int64_t i = threadIdx.x + c * THREADS;
+    if (r.h && i < quads)
+      store4<PAST != KEEP>(r.h + t * r.h_stride + 4 * i, make_float4(v[c][0], v[c][1], v[c][2], v[c][3]));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s = fma((double)v[c][e], (double)v[c][e], s);
+  }
+  for (int64_t i = threadIdx.x + C * THREADS; i < quads; i += THREADS) {
+    float x[4];
+    stream4<MODE, PAST == STREAM_ALL>(x, r, t, i);
+    if (r.h) store4<false>(r.h + t * r.h_stride + 4 * i, make_float4(x[0], x[1], x[2], x[3]));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s = fma((double)x[e], (double)x[e], s);
+  }
+  s = group_sum<64>(s);
+  if (THREADS > 64) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = part[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 64; ++w) s += part[w];
+  }
   const double inv = 1.0 / sqrt(s / (double)r.K + r.eps);
-  for (int64_t i = threadIdx.x; i < quads; i += kThreads) {
-    float v[4], g[4];
-    if (r.h) load4(v, r.h + t * r.h_stride + 4 * i);
-    else stream4<MODE>(v, r, t, i);
-    load4(g, r.gain + 4 * i);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (float)((double)v[e] * inv * (double)g[e]);
-    if (r.y) store4<false>(r.y + t * r.y_stride + 4 * i, make_float4(v[0], v[1], v[2], v[3]));
-    if (r.q) {
-      uint32_t codes;
-      const float scale = quantize4(v, codes);
-      r.q[t * quads + i] = codes;
-      if ((threadIdx.x & 7) == 0) r.d[(t * quads + i) >> 3] = scale;
-    }
+  for (int c = 0; c < C; ++c) {
+    const int64_t i = threadIdx.x + c * THREADS;
+    if (i < quads) put_normed<PAST != KEEP>(v[c], g[c], inv, r, t, i);
   }
+  for (int64_t i = threadIdx.x + C * THREADS; i < quads; i += THREADS) {
+    float x[4], gx[4];
+    if (r.h) load4(x, r.h + t * r.h_stride + 4 * i);
+    else stream4<MODE, PAST == STREAM_ALL>(x, r, t, i);
+    load4(gx, r.gain + 4 * i);
+    put_normed<false>(x, gx, inv, r, t, i);
+  }
+}
+
+// The weighted sum alone: quads [blockIdx.y * 256, ...) of a row.
+__global__ __launch_bounds__(kThreads) void combine_kernel(NormRows r, int64_t row0) {
+  const int64_t t = row0 + blockIdx.x, i = blockIdx.y * kThreads + threadIdx.x;
+  if (i >= r.K >> 2) return;
+  float v[4];
+  stream4<MODE_SUM, false>(v, r, t, i);
+  store4<false>(r.h + t * r.h_stride + 4 * i, make_float4(v[0], v[1], v[2], v[3]));
+}
+
+using RowKernel = void (*)(NormRows, int64_t);
+struct RowChoice {
+  RowKernel kernel;
+  int threads;
+};
+
+// As many threads as a row has quads to give each of them two or three (4096 values: 512
+// threads 3.2 us for one row, 1024 threads 3.2, 256 threads 4.0; 4096 rows of 5120: 512 x 3
+// 51.0 us, 256 x 5 53.0, 320 x 4 53.9, 64 x 20 on one wave 68 and more); what is longer than
+// 16384 values stays out of the registers (one row of 32768: 11.2 us; 17.0 with eight quads
+// a thread).
+template <int MODE, int PAST>
+RowChoice choose_row(int64_t quads) {
+  if (quads <= 256) return {row_norm_kernel<MODE, 256, 1, PAST>, 256};
+  if (quads <= 512) return {row_norm_kernel<MODE, 512, 1, PAST>, 512};
+  if (quads <= 1024) return {row_norm_kernel<MODE, 512, 2, PAST>, 512};
+  if (quads <= 1536) return {row_norm_kernel<MODE, 512, 3, PAST>, 512};
+  if (quads <= 2048) return {row_norm_kernel<MODE, 1024, 2, PAST>, 1024};
+  return {row_norm_kernel<MODE, 1024, 4, PAST>, 1024};
 }
 
 template <int MODE>
 hipError_t launch_rows(const NormRows& r, int64_t T, hipStream_t stream) {
-  for (int64_t t = 0; t < T; t += kMaxGrid) {
-    const int64_t n = std::min(T - t, kMaxGrid);
-    hipLaunchKernelGGL(row_norm_kernel<MODE>, dim3((uint32_t)n), dim3(kThreads), 0, stream, r, t);
+  const int64_t quads = r.K / 4;
+  // More than an XCD's 4 MB second-level cache of output goes past the caches (512 rows of 4096:
+  // 6.7 us so, 7.6 without; 300: 5.0 and 5.4; 150: 3.6 and 3.7).  Rows of 64 MB and more
+  // are read past them as well (4096 rows of 5120: 46.7 us so, 51.0 without; 2000 of 4096: 20.9
+  // and 18.2, where they are still in the last-level cache); the experts' rows never.
+  const int64_t values = T * r.K;
+  RowChoice c;
+  if (values < (1 << 20)) c = choose_row<MODE, KEEP>(quads);
+  else if (MODE == MODE_SUM || values < (1 << 24)) c = choose_row<MODE, STREAM_OUT>(quads);
+  else c = choose_row<MODE, MODE == MODE_SUM ? STREAM_OUT : STREAM_ALL>(quads);
+  const bool sum_alone = MODE == MODE_SUM && !r.gain;
+  const int64_t parts = sum_alone ? (quads + kThreads - 1) / kThreads : 1;
+  for (int64_t t = 0; t < T; t += kMaxGrid / parts) {
+    const int64_t n = std::min(T - t, kMaxGrid / parts);
+    if (sum_alone)
+      hipLaunchKernelGGL(combine_kernel, dim3((uint32_t)n, (uint32_t)parts), dim3(kThreads), 0,
+                         stream, r, t);
+    else
+      hipLaunchKernelGGL(c.kernel, dim3((uint32_t)n), dim3(c.threads), 0, stream, r, t);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int G, int C>
+hipError_t launch_heads(const float* x, int64_t T, int64_t H, int64_t D, int64_t x_stride,
+                        const float* gain, double eps, float* y, int64_t y_stride,
+                        hipStream_t stream) {
+  // One head a group of lanes: 2049 rows of 40 heads of 128 take 14.2 us (5.9 TB/s) and 14.7
+  // with four, one row 2.0 and 2.9.  Large outputs go past the caches (16.9 us without, at 64
+  // rows no difference).
+  const auto kernel =
+      T * H * D >= (1 << 20) ? rms_norm_kernel<G, C, true> : rms_norm_kernel<G, C, false>;
+  const int64_t per = kThreads / G, parts = std::min<int64_t>((H + per - 1) / per, 65535);
+  for (int64_t t = 0; t < T; t += kMaxGrid / parts) {
+    const int64_t n = std::min(T - t, kMaxGrid / parts);
+    for (int64_t h = 0; h < H; h += parts * per) {   // a launch holds 65535 workgroups along y
+      const int64_t m = std::min(parts, (H - h + per - 1) / per);
+      hipLaunchKernelGGL(kernel, dim3((uint32_t)n, (uint32_t)m), dim3(kThreads), 0, stream,
+                         x + t * x_stride + h * D, (int)(H - h), (int)D, x_stride, gain, eps,
+                         y + t * y_stride + h * D, y_stride);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   }
   return hipSuccess;
 }
@@ -135,21 +260,13 @@ hipError_t launch_rows(const NormRows& r, int64_t T, hipStream_t stream) {
 hipError_t launch_rms_norm(const float* x, int64_t T, int64_t H, int64_t D, int64_t x_stride,
                            const float* gain, double eps, float* y, int64_t y_stride,
                            hipStream_t stream) {
-  const int64_t per = kThreads / 64, groups = (H + per - 1) / per;
-  // a launch holds 2^32 threads at most and 65535 workgroups along y
-  const int64_t rows = std::max<int64_t>(1, kMaxGrid / groups);
-  for (int64_t t = 0; t < T; t += rows) {
-    const int64_t n = std::min(T - t, rows);
-    for (int64_t g = 0; g < groups; g += 65535) {
-      const int64_t m = std::min<int64_t>(groups - g, 65535), h = g * per;
-      hipLaunchKernelGGL(rms_norm_kernel, dim3((uint32_t)n, (uint32_t)m), dim3(kThreads), 0,
-                         stream, x + t * x_stride + h * D, (int)(H - h), (int)D, x_stride, gain,
-                         eps, y + t * y_stride + h * D, y_stride);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-  }
-  return hipSuccess;
+  const auto launch = D <= 32    ? launch_heads<8, 1>
+                      : D <= 64  ? launch_heads<16, 1>
+                      : D <= 128 ? launch_heads<32, 1>
+                      : D <= 256 ? launch_heads<64, 1>
+                      : D <= 512 ? launch_heads<64, 2>
+                                 : launch_heads<64, 4>;
+  return launch(x, T, H, D, x_stride, gain, eps, y, y_stride, stream);
 }
 
 hipError_t launch_add_rms_norm(const float* x, const float* add, int64_t T, int64_t K,
