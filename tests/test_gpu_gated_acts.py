@@ -42,6 +42,21 @@ def test_gate(M, K, act):
     assert np.array_equal(q, q3) and np.array_equal(d, d3)
 
 
+def test_codes_at_the_least_alignment():
+    """q and d 4 bytes off their allocations, at a size where codes are stored eight at a time."""
+    announce("quantize_gated_acts, alignment")
+    M, K = 1400, 1536
+    gu = torch.randn(M, 2 * K, device=device(), generator=torch.Generator(device()).manual_seed(5))
+    q, d = run(gu[:, :K], gu[:, K:], rf.GATE_SILU, M, K)
+    q1, d1 = torch.zeros(M * K + 8, dtype=torch.int8, device=device()), torch.zeros(M * K // 32 + 2, device=device())
+    rf.rfp2_quantize_gated_acts(gu[:, :K], gu[:, K:], M, K, rf.GATE_SILU, q1[4:-4], d1[1:-1])
+    assert np.array_equal(host(q1)[4:-4], q.reshape(-1)) and not host(q1)[:4].any() and not host(q1)[-4:].any()
+    assert np.array_equal(host(d1)[1:-1], d.reshape(-1)) and host(d1)[0] == 0 and host(d1)[-1] == 0
+    out = empty((M, K), torch.float32)
+    rf.rfp2_dequantize_acts(q1[4:-4], d1[1:-1], M, K, out)
+    assert np.array_equal(host(out), (q.reshape(M, -1, 32).astype(np.float32) * d[..., None]).reshape(M, K))
+
+
 @pytest.mark.parametrize("act", [rf.GATE_SILU, rf.GATE_GELU])
 def test_range_of_the_gate(act):
     """From gates that vanish to gates that pass, with other halves that bring them back into
