@@ -7,114 +7,341 @@
 //   w = scale * p, divided by the chosen p's sum where asked.
 //
 // Scores and choices are fp64: which of two experts is larger may hang on the last bit
-// of fp32 scores.  A logit of minus infinity masks its expert (v = -inf, p = 0).
+// of fp32 scores (of 4099 tokens over 256 experts with a bias, some do).  A logit of minus
+// infinity masks its expert.
+//
+// One wave a token.  Lane i holds experts i V .. i V + V - 1 and the best of those that are
+// left; a choice is a maximum over the wave and the lowest lane that holds it, which is
+// the lowest expert, and only that lane's best changes.  No sort, no LDS but for groups, whose
+// experts lie across lanes.  What is chosen without a bias needs no scores: logits are compared
+// as whole numbers, and only the chosen ones' exponentials are taken (all of them where a
+// softmax is not divided by the chosen ones' sum).  What bounds it is that chain of choices and the
+// launch for few tokens (1 over 128 experts 2.7 us, 1024 over 64 2.9), the vector
+// instructions for many (4099 over 256 with a bias 7.4 us, with groups 9.8: reading the logits
+// takes 0.7).
 #include <cmath>
+#include <type_traits>
 
+#include "acts_device.h"
 #include "rfp2_internal.h"
+#include "scores_device.h"
 
 namespace rfp2 {
 
 namespace {
 
-constexpr int kNone = 0x7FFFFFFF;
+struct Router {
+  const float* logits;
+  const float* bias;        // null: none
+  int32_t* ids;
+  float* weights;
+  int32_t* err;
+  double scale;
+  int64_t stride, T;
+  int32_t E, groups, group_top, top_groups, top_k;
+  int32_t per, shift;       // experts of a group; 2^shift lanes look at it, groups << shift <= 64
+  uint32_t group_magic;     // ceil(2^31 / (E / groups))
+  bool sigmoid, renorm;
+};
 
-// One wave a token; v [E] and p [E] in LDS.
-__global__ __launch_bounds__(64) void moe_route_kernel(
-    const float* __restrict__ logits, int64_t t0, int E, int64_t stride,
-    const float* __restrict__ bias, int sigmoid, int groups, int group_top, int top_groups,
-    int top_k, int renorm, double scale, int32_t* __restrict__ ids, float* __restrict__ weights,
-    int32_t* __restrict__ err) {
-  extern __shared__ double smem[];
-  double *v = smem, *p = smem + E;
-  __shared__ double value[64];
-  __shared__ int chosen[64];
-  const int lane = threadIdx.x;
-  const int64_t t = t0 + blockIdx.x;
-  const float* l = logits + t * stride;
+// What experts are compared by, the larger first: a logit's bits, or those of a score with
+// its bias, as a whole number in the order of the numbers.  Below every number: a mask
+// (chosen where nothing else is left), below that what is taken or was never there.
+constexpr uint32_t kGone = 0, kMasked = 1;
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);        // minus zero is zero
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t ordered(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x + 0.0);
+  return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ float number(uint32_t k) {
+  return __uint_as_float(k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u));
+}
+__device__ __forceinline__ double number(uint64_t k) {
+  return __builtin_bit_cast(double, k ^ (~(uint64_t)((int64_t)k >> 63) | 0x8000000000000000ull));
+}
 
-  float top = -INFINITY;
-  bool bad = false;
-  for (int e = lane; e < E; e += 64) {
-    const float x = l[e];
-    bad = bad || !(x < INFINITY) || (bias && !std::isfinite(bias[e]));
-    top = fmaxf(top, x);
-  }
-  for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-  if (__any(bad)) {                          // nothing can be said of this token
-    if (lane < top_k) {
-      ids[t * top_k + lane] = -1;
-      weights[t * top_k + lane] = __builtin_nanf("");
+// The largest over the wave.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t larger_of(uint32_t x) {
+  return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, ROWS == 0xF));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = larger_of<0xB1, 0xF>(x);               // neighbours
+  x = larger_of<0x4E, 0xF>(x);               // pairs
+  x = larger_of<0x141, 0xF>(x);              // the other four of eight
+  x = larger_of<0x140, 0xF>(x);              // the other eight of sixteen
+  x = larger_of<0x142, 0xA>(x);              // rows 1 and 3: the row before
+  x = larger_of<0x143, 0xC>(x);              // rows 2 and 3: the two before
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+// The lanes that hold the largest key.  Of 64 bits the upper half decides, and the lower
+// where several lanes share it.
+__device__ __forceinline__ uint64_t lanes_of_largest(uint32_t k) {
+  return __ballot(k == wave_max(k));
+}
+__device__ __forceinline__ uint64_t lanes_of_largest(uint64_t k) {
+  const uint32_t hi = (uint32_t)(k >> 32), lo = (uint32_t)k;
+  const bool top = hi == wave_max(hi);
+  const uint64_t lanes = __ballot(top);
+  if ((lanes & (lanes - 1)) == 0) return lanes;
+  const uint32_t most = wave_max(top ? lo : 0u);
+  return __ballot(top && lo == most);
+}
+
+// Scores before they are divided by the softmax's sum; what exp(-690) is more than counts as
+// 0.  Without branches, so that the V chains of one lane run side by side.
+template <int V>
+__device__ __forceinline__ void scores(double (&p)[V], const float (&x)[V], float top,
+                                       bool sigmoid) {
+  if (sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      p[i] = logistic(__builtin_amdgcn_fmed3f(x[i], -690.0f, 690.0f));
+      p[i] = x[i] >= -690.0f ? p[i] : 0.0;
     }
-    if (lane == 0 && err) *err = 1;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const double d = (double)x[i] - (double)top;
+      p[i] = exp_f64(fmax(d, -690.0));
+      p[i] = d >= -690.0 ? p[i] : 0.0;       // not for NaN: all are minus infinity
+    }
+  }
+}
+
+template <class K>
+__device__ __forceinline__ K larger(K a, K b) { return a > b ? a : b; }
+template <class K>
+__device__ __forceinline__ K smaller(K a, K b) { return a < b ? a : b; }
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t other(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ uint64_t other(uint64_t x) {
+  return (uint64_t)other<CTRL>((uint32_t)(x >> 32)) << 32 | other<CTRL>((uint32_t)x);
+}
+__device__ __forceinline__ uint32_t of_lane(uint32_t x, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
+}
+__device__ __forceinline__ uint64_t of_lane(uint64_t x, int lane) {
+  return (uint64_t)of_lane((uint32_t)(x >> 32), lane) << 32 | of_lane((uint32_t)x, lane);
+}
+
+// 2^shift lanes look at a group's experts; true for the lanes whose group stays.
+template <class K>
+__device__ __forceinline__ bool group_stays(const K* key, const Router& r) {
+  const int lane = threadIdx.x & 63, lanes = 1 << r.shift;
+  const int g = lane >> r.shift;
+  K a = kGone, b = kGone;                    // the two largest
+  if (g < r.groups)
+    for (int e = lane & (lanes - 1); e < r.per; e += lanes) {
+      const K x = key[g * r.per + e];
+      b = larger(b, smaller(x, a));
+      a = larger(a, x);
+    }
+  const auto join = [&](K oa, K ob) {
+    b = larger(larger(b, ob), smaller(a, oa));
+    a = larger(a, oa);
+  };
+  if (lanes >= 2) join(other<0xB1>(a), other<0xB1>(b));
+  if (lanes >= 4) join(other<0x4E>(a), other<0x4E>(b));
+  if (lanes >= 8) join(other<0x141>(a), other<0x141>(b));
+  if (lanes >= 16) join(other<0x140>(a), other<0x140>(b));
+  if (lanes >= 32) join(__shfl_xor(a, 16, 64), __shfl_xor(b, 16, 64));
+  if (r.group_top == 2 && b > kMasked) a = ordered(number(a) + number(b));
+  int before = 0;
+  for (int o = 0; o < r.groups; ++o) {
+    const K x = of_lane(a, o << r.shift);
+    before += x > a || (x == a && o < g);
+  }
+  return g < r.groups && before < r.top_groups;
+}
+
+// A lane's V keys: its largest, where it was among the V (the first of equals), and how to
+// take it away.  Up to eight are sorted once and move up (by neighbours' exchanges, which leave
+// equals in their order); more are looked through each time.
+template <int V, class K>
+struct Held {
+  K key[V];
+  int at[V];
+  __device__ __forceinline__ explicit Held(const K (&k)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      key[i] = k[i];
+      at[i] = i;
+    }
+#pragma unroll
+    for (int round = 0; round < V; ++round)
+#pragma unroll
+      for (int i = round & 1; i + 1 < V; i += 2) {
+        const bool swap = key[i + 1] > key[i];
+        const K a = key[i], b = key[i + 1];
+        const int pa = at[i], pb = at[i + 1];
+        key[i] = swap ? b : a;
+        key[i + 1] = swap ? a : b;
+        at[i] = swap ? pb : pa;
+        at[i + 1] = swap ? pa : pb;
+      }
+  }
+  __device__ __forceinline__ K best() const { return key[0]; }
+  __device__ __forceinline__ int place() const { return at[0]; }
+  __device__ __forceinline__ void take(bool mine) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      key[i] = mine ? (i + 1 < V ? key[(i + 1) % V] : (K)kGone) : key[i];
+      if (i + 1 < V) at[i] = mine ? at[(i + 1) % V] : at[i];
+    }
+  }
+};
+template <int V, class K>
+struct Searched {
+  K key[V], top;
+  int at;
+  __device__ __forceinline__ explicit Searched(const K (&k)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = k[i];
+    look();
+  }
+  __device__ __forceinline__ void look() {
+    top = key[0];
+    at = 0;
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+      if (key[i] > top) {
+        top = key[i];
+        at = i;
+      }
+  }
+  __device__ __forceinline__ K best() const { return top; }
+  __device__ __forceinline__ int place() const { return at; }
+  __device__ __forceinline__ void take(bool mine) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (mine && i == at) key[i] = kGone;
+    look();
+  }
+};
+template <class K>
+struct Held<16, K> : Searched<16, K> {
+  using Searched<16, K>::Searched;
+};
+template <class K>
+struct Held<32, K> : Searched<32, K> {
+  using Searched<32, K>::Searched;
+};
+
+template <int V, bool BIAS>
+__global__ __launch_bounds__(256) void moe_route_kernel(Router r, int64_t t0) {
+  using K = std::conditional_t<BIAS, uint64_t, uint32_t>;
+  extern __shared__ double smem[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = t0 + blockIdx.x * (int64_t)(blockDim.x >> 6) + wave;
+  if (t >= r.T) return;                      // waves do not wait for each other
+  const float* l = r.logits + t * r.stride;
+
+  float x[V], bias[V];                       // past the last expert: the last, masked
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = l[min(lane * V + i, r.E - 1)];
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = r.bias[min(lane * V + i, r.E - 1)];
+  }
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    bad = bad || !(x[i] < INFINITY);
+    if constexpr (BIAS) bad = bad || !(fabsf(bias[i]) < INFINITY);
+    if (lane * V + i >= r.E) x[i] = -INFINITY;
+  }
+  if (__any(bad)) {                          // nothing can be said of this token
+    if (lane < r.top_k) {
+      r.ids[t * r.top_k + lane] = -1;
+      r.weights[t * r.top_k + lane] = __builtin_nanf("");
+    }
+    if (lane == 0 && r.err) *r.err = 1;
     return;
   }
-  double sum = 0.0;
-  for (int e = lane; e < E; e += 64) {
-    const double x = l[e];
-    const double s = x == -INFINITY ? 0.0 : sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)top);
-    p[e] = s;
-    sum += s;
+
+  float top = 0.0f;
+  double share = 1.0;
+  if (!r.sigmoid) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = max(m, ordered(x[i]));
+    top = number(wave_max(m));
   }
-  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  const double share = sigmoid || sum == 0.0 ? 1.0 : 1.0 / sum;
-  for (int e = lane; e < E; e += 64) {
-    p[e] *= share;
-    v[e] = l[e] == -INFINITY ? -INFINITY : bias ? p[e] + (double)bias[e] : (double)l[e];
-  }
-  __syncthreads();
-  if (groups > 1) {
-    const int per = E / groups;
-    if (lane < groups) {
-      double a = -INFINITY, b = -INFINITY;   // the two largest
-      for (int e = lane * per; e < (lane + 1) * per; ++e) {
-        b = fmax(b, fmin(a, v[e]));
-        a = fmax(a, v[e]);
-      }
-      value[lane] = group_top == 2 && b != -INFINITY ? a + b : a;
+  double p[V];
+  if (BIAS || (!r.sigmoid && !r.renorm)) {
+    scores<V>(p, x, top, r.sigmoid);
+    if (!r.sigmoid) {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += p[i];
+      sum = group_sum<64>(sum);
+      share = sum > 0.0 ? reciprocal(sum) : 0.0;
     }
-    __syncthreads();
-    if (lane < groups) {
-      int before = 0;
-      for (int g = 0; g < groups; ++g)
-        before += value[g] > value[lane] || (value[g] == value[lane] && g < lane);
-      if (before >= top_groups)
-        for (int e = lane * per; e < (lane + 1) * per; ++e) v[e] = __builtin_nan("");
+  }
+  K key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if constexpr (BIAS) key[i] = ordered(p[i] * share + (double)bias[i]);
+    else key[i] = ordered(x[i]);
+    if (x[i] == -INFINITY) key[i] = lane * V + i < r.E ? kMasked : kGone;
+  }
+
+  if (r.groups > 1) {
+    K* mine = reinterpret_cast<K*>(smem) + wave * r.E;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane * V + i < r.E) mine[lane * V + i] = key[i];
+    // a wave's LDS operations are done in their order; the compiler has to keep it
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const uint64_t stays = __ballot(group_stays(mine, r));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t g = __umulhi(2u * (lane * V + i), r.group_magic);
+      if (!((stays >> ((g << r.shift) & 63)) & 1)) key[i] = kGone;
     }
-    __syncthreads();
   }
-  for (int j = 0; j < top_k; ++j) {          // NaN: taken, or not to be had
-    double best = -INFINITY;
-    int at = kNone;
-    for (int e = lane; e < E; e += 64)
-      if (v[e] > best || (v[e] == best && e < at)) {
-        best = v[e];
-        at = e;
-      }
-    for (int o = 32; o >= 1; o >>= 1) {
-      const double ob = __shfl_xor(best, o, 64);
-      const int oa = __shfl_xor(at, o, 64);
-      if (ob > best || (ob == best && oa < at)) {
-        best = ob;
-        at = oa;
-      }
-    }
-    if (lane == 0) {
-      chosen[j] = at;
-      v[at] = __builtin_nan("");
-    }
-    __syncthreads();
+
+  Held<V, K> held(key);
+  int id = 0;                                // lane j: choice j
+  for (int j = 0; j < r.top_k; ++j) {
+    const int from = __builtin_ctzll(lanes_of_largest(held.best()));
+    const int chosen = from * V + __builtin_amdgcn_readlane(held.place(), from);
+    if (lane == j) id = chosen;
+    held.take(lane == from);
   }
-  const int id = lane < top_k ? chosen[lane] : 0;
-  double w = lane < top_k ? p[id] : 0.0;
-  if (renorm) {
-    double total = w;
-    for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o, 64);
-    w = total > 0.0 ? w / total : 0.0;
+
+  double w = 0.0;
+  if (lane < r.top_k) {
+    const float mine[1] = {l[id]};
+    double s[1];
+    scores<1>(s, mine, top, r.sigmoid);
+    w = s[0] * share;
   }
-  if (lane < top_k) {
-    ids[t * top_k + lane] = id;
-    weights[t * top_k + lane] = (float)(scale * w);
+  if (r.renorm) {
+    const double total = group_sum<64>(w);
+    w = total > 0.0 ? w * reciprocal(total) : 0.0;
   }
+  if (lane < r.top_k) {
+    r.ids[t * r.top_k + lane] = id;
+    r.weights[t * r.top_k + lane] = (float)(r.scale * w);
+  }
+}
+
+template <int V>
+void enqueue(const Router& r, int64_t t, uint32_t grid, int waves, size_t lds,
+             hipStream_t stream) {
+  const auto kernel = r.bias ? moe_route_kernel<V, true> : moe_route_kernel<V, false>;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * waves), lds, stream, r, t);
 }
 
 }  // namespace
@@ -123,11 +350,22 @@ hipError_t launch_moe_route(const float* logits, int64_t T, int64_t E, int64_t s
                             const float* bias, bool sigmoid, int groups, int group_top,
                             int top_groups, int top_k, bool renorm, double scale, int32_t* ids,
                             float* weights, int32_t* err, hipStream_t stream) {
+  int shift = 6;
+  while (groups << shift > 64) --shift;
+  const int64_t per = E / groups;
+  const Router r = {logits, bias, ids, weights, err, scale, stride, T, (int32_t)E, groups,
+                    group_top, top_groups, top_k, (int32_t)per, shift,
+                    (uint32_t)(((int64_t(1) << 31) + per - 1) / per), sigmoid, renorm};
+  const int waves = T >= 1024 && E <= 512 ? 4 : 1;
+  const size_t lds = groups > 1 ? (size_t)waves * E * sizeof(double) : 0;   // at most 16 KiB
   for (int64_t t = 0; t < T; t += kMaxGrid) {
-    hipLaunchKernelGGL(moe_route_kernel, dim3((uint32_t)std::min(T - t, kMaxGrid)), dim3(64),
-                       16 * (size_t)E, stream, logits, t, (int)E, stride, bias, sigmoid ? 1 : 0,
-                       groups, group_top, top_groups, top_k, renorm ? 1 : 0, scale, ids, weights,
-                       err);
+    const uint32_t grid = (uint32_t)((std::min(T - t, kMaxGrid) + waves - 1) / waves);
+    if (E <= 64) enqueue<1>(r, t, grid, waves, lds, stream);
+    else if (E <= 128) enqueue<2>(r, t, grid, waves, lds, stream);
+    else if (E <= 256) enqueue<4>(r, t, grid, waves, lds, stream);
+    else if (E <= 512) enqueue<8>(r, t, grid, waves, lds, stream);
+    else if (E <= 1024) enqueue<16>(r, t, grid, waves, lds, stream);
+    else enqueue<32>(r, t, grid, waves, lds, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

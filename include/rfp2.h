@@ -565,7 +565,8 @@ rfp2_status rfp2_moe_combine(const float* x, const float* rows, const float* wei
  *   group_top (1 or 2) largest v (by those that are not masked), and only the
  *   top_groups best groups stay.  The top_k largest v among what stays are
  *   chosen, in falling order; among equal groups or experts the lower comes
- *   first.  v and p are fp64.
+ *   first.  v and p are fp64 (a sigmoid's logit, or one less the token's largest
+ *   in a softmax, below -690 makes p 0).
  *   ids     [T][top_k] int32, 4-byte aligned.
  *   weights [T][top_k] fp32, 4-byte aligned: scale * p of the chosen, where
  *          renorm != 0 divided by the sum of the chosen p (0 where that is 0).

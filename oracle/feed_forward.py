@@ -44,12 +44,13 @@ def gated(g, u, gelu):
 
 
 def scores(logits, sigmoid):
-    """One token's scores; a logit of minus infinity scores 0."""
+    """One token's scores; a logit of minus infinity scores 0, and so does one whose
+    exponential is below exp(-690)."""
     l = [float(x) for x in logits]
     if sigmoid:
-        return [0.0 if x < -700.0 else 1.0 / (1.0 + math.exp(-x)) for x in l]
+        return [0.0 if x < -690.0 else 1.0 / (1.0 + math.exp(-x)) for x in l]
     top = max(l)
-    e = [0.0 if x == -math.inf else math.exp(x - top) for x in l]
+    e = [0.0 if x == -math.inf or x - top < -690.0 else math.exp(x - top) for x in l]
     total = math.fsum(e)
     return [x / total if total else 0.0 for x in e]
 

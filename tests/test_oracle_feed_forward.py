@@ -60,6 +60,7 @@ def test_scores():
     assert ff.scores([-math.inf, 5.0], False) == [0.0, 1.0]
     assert ff.scores([-math.inf, -math.inf], False) == [0.0, 0.0]
     assert np.allclose(ff.scores([0.0, math.log(3.0), -math.inf, -1e30], True), [0.5, 0.75, 0.0, 0.0])
+    assert ff.scores([0.0, -690.0, -690.5], False)[2] == 0.0 < ff.scores([0.0, -690.0, -690.5], False)[1]
 
 
 def test_route_by_hand():
