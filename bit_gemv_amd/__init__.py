@@ -11,6 +11,7 @@ if librfp2.so is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 
@@ -131,11 +132,11 @@ def header_symbols() -> list[str]:
 # ---------------------------------------------------------------------------
 # marshalling helpers
 # ---------------------------------------------------------------------------
-def _stream(stream):
+def _stream(stream, gpu=None):
     import torch
     if stream is None:
         # the handle without a Stream object around it: 0.3 us against 2.9, in every call
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice() if gpu is None else gpu)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -526,35 +527,58 @@ def rfp2_paged_attn(cache, q, B: int, new_tokens: int, H: int, lens, scale: floa
         _ptr(workspace, torch.uint8, 0, "workspace"), workspace.numel(), _stream(stream)))
 
 
-def _here(*tensors):
-    """Every tensor that is there on the GPU whose stream the call goes to."""
+def _gpu() -> int:
+    """The GPU whose stream a call goes to (none: no tensor is on it)."""
     import torch
-    gpu = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != gpu:
-            raise ValueError(f"a tensor of the call is on {t.device}, the current GPU is cuda:{gpu}")
+    try:
+        return torch._C._cuda_getDevice()
+    except RuntimeError:
+        return -2
+
+
+def _at(t, dtype, shape: tuple, gpu: int, name: str):
+    """Device pointer of a tensor that the call touches all of (None for None).  One of just
+    this shape, as most are, is looked at no further (0.3 us); a longer one, or one of
+    another shape, only has to hold as many values, contiguous."""
+    if t is None:
+        return None
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == gpu
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:                     # no tensor: _ptr says so
+        pass
+    p = _ptr(t, dtype, math.prod(shape), name)
+    if t.get_device() != gpu:
+        raise ValueError(f"{name} is on {t.device}, the current GPU is cuda:{gpu}")
+    return p
+
+
+def _rows_at(t, dtype, shape: tuple, gpu: int, name: str):
+    """_rows for T rows of a width (shape), or (None, 0): the same shortcut."""
+    if t is None:
+        return None, 0
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == gpu
+                and t.is_contiguous()):
+            return t.data_ptr(), shape[1]
+    except AttributeError:                     # no tensor: _rows says so
+        pass
+    p, stride = _rows(t, shape[0], shape[1], name)
+    if t.get_device() != gpu:
+        raise ValueError(f"{name} is on {t.device}, the current GPU is cuda:{gpu}")
+    return p, stride
 
 
 def rfp2_rms_norm(x, T: int, H: int, D: int, gain, eps: float, y, stream=None) -> None:
     """x, y: T rows of H * D values ([T, H, D] or [T, H * D]); rows may lie
     apart.  y may be x."""
     import torch
-    xp, xs = _rows(x, T, H * D, "x")
-    yp, ys = _rows(y, T, H * D, "y")
-    gp = _ptr(gain, torch.float32, D, "gain")
-    _here(x, y, gain)
-    _check("rfp2_rms_norm", lib().rfp2_rms_norm(xp, T, H, D, xs, gp, eps, yp, ys,
-                                                _stream(stream)))
-
-
-def _norm_out(T: int, K: int, h, y, q, d):
-    """Pointers and strides of what a norm of rows writes (None: not wanted)."""
-    import torch
-    hp, hs = (None, 0) if h is None else _rows(h, T, K, "h")
-    yp, ys = (None, 0) if y is None else _rows(y, T, K, "y")
-    qp = None if q is None else _ptr(q, torch.int8, T * K, "q")
-    dp = None if d is None else _ptr(d, torch.float32, T * _blocks(K), "d")
-    return hp, hs, yp, ys, qp, dp
+    f32, gpu, shape = torch.float32, _gpu(), (T, H * D)
+    xp, xs = _rows_at(x, f32, shape, gpu, "x")
+    yp, ys = _rows_at(y, f32, shape, gpu, "y")
+    _check("rfp2_rms_norm", lib().rfp2_rms_norm(
+        xp, T, H, D, xs, _at(gain, f32, (D,), gpu, "gain"), eps, yp, ys, _stream(stream, gpu)))
 
 
 def rfp2_add_rms_norm(x, add, T: int, K: int, gain, eps: float, h=None, y=None, q=None, d=None,
@@ -562,13 +586,15 @@ def rfp2_add_rms_norm(x, add, T: int, K: int, gain, eps: float, h=None, y=None, 
     """x, add, h, y: T rows of K values; rows may lie apart.  add and h, y, or q
     and d may be None; h and y may each be x or add."""
     import torch
-    xp, xs = _rows(x, T, K, "x")
-    ap, as_ = (None, 0) if add is None else _rows(add, T, K, "add")
-    gp = _ptr(gain, torch.float32, K, "gain")
-    hp, hs, yp, ys, qp, dp = _norm_out(T, K, h, y, q, d)
-    _here(x, add, gain, h, y, q, d)
+    f32, gpu, shape = torch.float32, _gpu(), (T, K)
+    xp, xs = _rows_at(x, f32, shape, gpu, "x")
+    ap, as_ = _rows_at(add, f32, shape, gpu, "add")
+    hp, hs = _rows_at(h, f32, shape, gpu, "h")
+    yp, ys = _rows_at(y, f32, shape, gpu, "y")
     _check("rfp2_add_rms_norm", lib().rfp2_add_rms_norm(
-        xp, ap, T, K, xs, as_, gp, eps, hp, hs, yp, ys, qp, dp, _stream(stream)))
+        xp, ap, T, K, xs, as_, _at(gain, f32, (K,), gpu, "gain"), eps, hp, hs, yp, ys,
+        _at(q, torch.int8, shape, gpu, "q"), _at(d, f32, (T, _blocks(K)), gpu, "d"),
+        _stream(stream, gpu)))
 
 
 def rfp2_moe_combine(x, rows, weights, T: int, top_k: int, K: int, h=None, gain=None,
@@ -577,14 +603,16 @@ def rfp2_moe_combine(x, rows, weights, T: int, top_k: int, K: int, h=None, gain=
     weights: [T, top_k], contiguous.  x may be None; without a gain only h is
     written."""
     import torch
-    xp, xs = (None, 0) if x is None else _rows(x, T, K, "x")
-    rp = _ptr(rows, torch.float32, T * top_k * K, "rows")
-    wp = _ptr(weights, torch.float32, T * top_k, "weights")
-    gp = None if gain is None else _ptr(gain, torch.float32, K, "gain")
-    hp, hs, yp, ys, qp, dp = _norm_out(T, K, h, y, q, d)
-    _here(x, rows, weights, gain, h, y, q, d)
+    f32, gpu, shape = torch.float32, _gpu(), (T, K)
+    xp, xs = _rows_at(x, f32, shape, gpu, "x")
+    hp, hs = _rows_at(h, f32, shape, gpu, "h")
+    yp, ys = _rows_at(y, f32, shape, gpu, "y")
     _check("rfp2_moe_combine", lib().rfp2_moe_combine(
-        xp, rp, wp, T, top_k, K, xs, gp, eps, hp, hs, yp, ys, qp, dp, _stream(stream)))
+        xp, _at(rows, f32, (T, top_k, K), gpu, "rows"),
+        _at(weights, f32, (T, top_k), gpu, "weights"), T, top_k, K, xs,
+        _at(gain, f32, (K,), gpu, "gain"), eps, hp, hs, yp, ys,
+        _at(q, torch.int8, shape, gpu, "q"), _at(d, f32, (T, _blocks(K)), gpu, "d"),
+        _stream(stream, gpu)))
 
 
 def rfp2_moe_route(logits, T: int, E: int, bias, score: int, groups: int, group_top: int,
@@ -592,36 +620,32 @@ def rfp2_moe_route(logits, T: int, E: int, bias, score: int, groups: int, group_
                    err=None, stream=None) -> None:
     """logits: T rows of E values; rows may lie apart.  bias may be None."""
     import torch
-    lp, ls = _rows(logits, T, E, "logits")
-    bp = None if bias is None else _ptr(bias, torch.float32, E, "bias")
-    ip = _ptr(ids, torch.int32, T * top_k, "ids")
-    wp = _ptr(weights, torch.float32, T * top_k, "weights")
-    errp = None if err is None else _ptr(err, torch.int32, 1, "err")
-    _here(logits, bias, ids, weights, err)
+    f32, gpu, shape = torch.float32, _gpu(), (T, top_k)
+    lp, ls = _rows_at(logits, f32, (T, E), gpu, "logits")
     _check("rfp2_moe_route", lib().rfp2_moe_route(
-        lp, T, E, ls, bp, score, groups, group_top, top_groups, top_k, bool(renorm), scale, ip, wp,
-        errp, _stream(stream)))
+        lp, T, E, ls, _at(bias, f32, (E,), gpu, "bias"), score, groups, group_top, top_groups,
+        top_k, 1 if renorm else 0, scale, _at(ids, torch.int32, shape, gpu, "ids"),
+        _at(weights, f32, shape, gpu, "weights"), _at(err, torch.int32, (1,), gpu, "err"),
+        _stream(stream, gpu)))
 
 
 def rfp2_quantize_gated_acts(gate, up, M: int, K: int, act: int, q, d, stream=None) -> None:
     """gate, up: M rows of K values; rows may lie apart (two halves of one product)."""
     import torch
-    gp, gs = _rows(gate, M, K, "gate")
-    up_, us = _rows(up, M, K, "up")
-    qp = _ptr(q, torch.int8, M * K, "q")
-    dp = _ptr(d, torch.float32, M * _blocks(K), "d")
-    _here(gate, up, q, d)
+    f32, gpu, shape = torch.float32, _gpu(), (M, K)
+    gp, gs = _rows_at(gate, f32, shape, gpu, "gate")
+    up_, us = _rows_at(up, f32, shape, gpu, "up")
     _check("rfp2_quantize_gated_acts", lib().rfp2_quantize_gated_acts(
-        gp, up_, M, K, gs, us, act, qp, dp, _stream(stream)))
+        gp, up_, M, K, gs, us, act, _at(q, torch.int8, shape, gpu, "q"),
+        _at(d, f32, (M, _blocks(K)), gpu, "d"), _stream(stream, gpu)))
 
 
 def rfp2_dequantize_acts(q, d, M: int, K: int, a, stream=None) -> None:
     import torch
-    qp = _ptr(q, torch.int8, M * K, "q")
-    dp = _ptr(d, torch.float32, M * _blocks(K), "d")
-    ap = _ptr(a, torch.float32, M * K, "a")
-    _here(q, d, a)
-    _check("rfp2_dequantize_acts", lib().rfp2_dequantize_acts(qp, dp, M, K, ap, _stream(stream)))
+    f32, gpu, shape = torch.float32, _gpu(), (M, K)
+    _check("rfp2_dequantize_acts", lib().rfp2_dequantize_acts(
+        _at(q, torch.int8, shape, gpu, "q"), _at(d, f32, (M, _blocks(K)), gpu, "d"), M, K,
+        _at(a, f32, shape, gpu, "a"), _stream(stream, gpu)))
 
 
 def rfp2_debug_decode(w, N: int, K: int, codes_out, scales_out, stream=None) -> None:
