@@ -559,9 +559,10 @@ def _rows_at(t, dtype, shape: tuple, gpu: int, name: str):
     if t is None:
         return None, 0
     try:
-        if (t.dtype is dtype and t.shape == shape and t.get_device() == gpu
-                and t.is_contiguous()):
-            return t.data_ptr(), shape[1]
+        if t.dtype is dtype and t.shape == shape and t.get_device() == gpu:
+            stride, one = t.stride()
+            if one == 1:
+                return t.data_ptr(), stride if shape[0] > 1 else shape[1]
     except AttributeError:                     # no tensor: _rows says so
         pass
     p, stride = _rows(t, shape[0], shape[1], name)

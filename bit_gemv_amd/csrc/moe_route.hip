@@ -37,12 +37,15 @@ struct Router {
   float* weights;
   int32_t* err;
   double scale;
-  int64_t stride, T;
-  int32_t E, groups, group_top, top_groups, top_k;
+  int64_t stride;
+  int32_t T, E, groups, group_top, top_groups, top_k;
+  int32_t waves;            // of a workgroup
   int32_t per, shift;       // experts of a group; 2^shift lanes look at it, groups << shift <= 64
   uint32_t group_magic;     // ceil(2^31 / (E / groups))
   bool sigmoid, renorm;
 };
+// Larger arguments, or blockDim in a kernel, cost the host 0.7 us a launch.
+static_assert(sizeof(Router) <= 112, "");
 
 // What experts are compared by, the larger first: a logit's bits, or those of a score with
 // its bias, as a whole number in the order of the numbers.  Below every number: a mask
@@ -237,11 +240,11 @@ struct Held<32, K> : Searched<32, K> {
 };
 
 template <int V, bool BIAS>
-__global__ __launch_bounds__(256) void moe_route_kernel(Router r, int64_t t0) {
+__global__ __launch_bounds__(256) void moe_route_kernel(Router r) {
   using K = std::conditional_t<BIAS, uint64_t, uint32_t>;
   extern __shared__ double smem[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = t0 + blockIdx.x * (int64_t)(blockDim.x >> 6) + wave;
+  const int64_t t = blockIdx.x * r.waves + wave;
   if (t >= r.T) return;                      // waves do not wait for each other
   const float* l = r.logits + t * r.stride;
 
@@ -338,10 +341,10 @@ __global__ __launch_bounds__(256) void moe_route_kernel(Router r, int64_t t0) {
 }
 
 template <int V>
-void enqueue(const Router& r, int64_t t, uint32_t grid, int waves, size_t lds,
-             hipStream_t stream) {
+void enqueue(const Router& r, size_t lds, hipStream_t stream) {
   const auto kernel = r.bias ? moe_route_kernel<V, true> : moe_route_kernel<V, false>;
-  hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * waves), lds, stream, r, t);
+  hipLaunchKernelGGL(kernel, dim3((r.T + r.waves - 1) / r.waves), dim3(64 * r.waves), lds, stream,
+                     r);
 }
 
 }  // namespace
@@ -352,20 +355,21 @@ hipError_t launch_moe_route(const float* logits, int64_t T, int64_t E, int64_t s
                             float* weights, int32_t* err, hipStream_t stream) {
   int shift = 6;
   while (groups << shift > 64) --shift;
-  const int64_t per = E / groups;
-  const Router r = {logits, bias, ids, weights, err, scale, stride, T, (int32_t)E, groups,
-                    group_top, top_groups, top_k, (int32_t)per, shift,
-                    (uint32_t)(((int64_t(1) << 31) + per - 1) / per), sigmoid, renorm};
-  const int waves = T >= 1024 && E <= 512 ? 4 : 1;
+  const int32_t per = (int32_t)E / groups;
+  // Few tokens: a wave a workgroup, more compute units for them.
+  const int32_t waves = T >= 1024 && E <= 512 ? 4 : 1;
   const size_t lds = groups > 1 ? (size_t)waves * E * sizeof(double) : 0;   // at most 16 KiB
   for (int64_t t = 0; t < T; t += kMaxGrid) {
-    const uint32_t grid = (uint32_t)((std::min(T - t, kMaxGrid) + waves - 1) / waves);
-    if (E <= 64) enqueue<1>(r, t, grid, waves, lds, stream);
-    else if (E <= 128) enqueue<2>(r, t, grid, waves, lds, stream);
-    else if (E <= 256) enqueue<4>(r, t, grid, waves, lds, stream);
-    else if (E <= 512) enqueue<8>(r, t, grid, waves, lds, stream);
-    else if (E <= 1024) enqueue<16>(r, t, grid, waves, lds, stream);
-    else enqueue<32>(r, t, grid, waves, lds, stream);
+    const Router r = {logits + t * stride, bias, ids + t * top_k, weights + t * top_k, err, scale,
+                      stride, (int32_t)std::min(T - t, kMaxGrid), (int32_t)E, groups, group_top,
+                      top_groups, top_k, waves, per, shift,
+                      (uint32_t)(((int64_t(1) << 31) + per - 1) / per), sigmoid, renorm};
+    if (E <= 64) enqueue<1>(r, lds, stream);
+    else if (E <= 128) enqueue<2>(r, lds, stream);
+    else if (E <= 256) enqueue<4>(r, lds, stream);
+    else if (E <= 512) enqueue<8>(r, lds, stream);
+    else if (E <= 1024) enqueue<16>(r, lds, stream);
+    else enqueue<32>(r, lds, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
