@@ -48,9 +48,10 @@ struct Router {
 static_assert(sizeof(Router) <= 112, "");
 
 // What experts are compared by, the larger first: a logit's bits, or those of a score with
-// its bias, as a whole number in the order of the numbers.  Below every number: a mask
-// (chosen where nothing else is left), below that what is taken or was never there.
-constexpr uint32_t kGone = 0, kMasked = 1;
+// its bias, as a whole number in the order of the numbers.  The lowest number's is that of
+// minus infinity, a mask (chosen where nothing else is left); below it what is taken or was never
+// there.
+constexpr uint32_t kGone = 0;
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);        // minus zero is zero
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
@@ -62,10 +63,6 @@ __device__ __forceinline__ uint64_t ordered(double x) {
 __device__ __forceinline__ float number(uint32_t k) {
   return __uint_as_float(k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u));
 }
-__device__ __forceinline__ double number(uint64_t k) {
-  return __builtin_bit_cast(double, k ^ (~(uint64_t)((int64_t)k >> 63) | 0x8000000000000000ull));
-}
-
 // The largest over the wave.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t larger_of(uint32_t x) {
@@ -116,39 +113,45 @@ __device__ __forceinline__ void scores(double (&p)[V], const float (&x)[V], floa
   }
 }
 
-template <class K>
-__device__ __forceinline__ K larger(K a, K b) { return a > b ? a : b; }
-template <class K>
-__device__ __forceinline__ K smaller(K a, K b) { return a < b ? a : b; }
-
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
 template <int CTRL>
-__device__ __forceinline__ uint32_t other(uint32_t x) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
+__device__ __forceinline__ float other(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
 }
 template <int CTRL>
-__device__ __forceinline__ uint64_t other(uint64_t x) {
-  return (uint64_t)other<CTRL>((uint32_t)(x >> 32)) << 32 | other<CTRL>((uint32_t)x);
+__device__ __forceinline__ double other(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
-__device__ __forceinline__ uint32_t of_lane(uint32_t x, int lane) {
-  return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
+__device__ __forceinline__ float of_lane(float x, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
 }
-__device__ __forceinline__ uint64_t of_lane(uint64_t x, int lane) {
-  return (uint64_t)of_lane((uint32_t)(x >> 32), lane) << 32 | of_lane((uint32_t)x, lane);
+__device__ __forceinline__ double of_lane(double x, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(b >> 32), lane);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// 2^shift lanes look at a group's experts; true for the lanes whose group stays.
-template <class K>
-__device__ __forceinline__ bool group_stays(const K* key, const Router& r) {
+// 2^shift lanes look at a group's experts (minus infinity: masked); true for the lanes whose
+// group stays.
+template <class F>
+__device__ __forceinline__ bool group_stays(const F* v, const Router& r) {
   const int lane = threadIdx.x & 63, lanes = 1 << r.shift;
   const int g = lane >> r.shift;
-  K a = kGone, b = kGone;                    // the two largest
+  F a = -INFINITY, b = -INFINITY;            // the two largest
   if (g < r.groups)
     for (int e = lane & (lanes - 1); e < r.per; e += lanes) {
-      const K x = key[g * r.per + e];
+      const F x = v[g * r.per + e];
       b = larger(b, smaller(x, a));
       a = larger(a, x);
     }
-  const auto join = [&](K oa, K ob) {
+  const auto join = [&](F oa, F ob) {
     b = larger(larger(b, ob), smaller(a, oa));
     a = larger(a, oa);
   };
@@ -157,10 +160,10 @@ __device__ __forceinline__ bool group_stays(const K* key, const Router& r) {
   if (lanes >= 8) join(other<0x141>(a), other<0x141>(b));
   if (lanes >= 16) join(other<0x140>(a), other<0x140>(b));
   if (lanes >= 32) join(__shfl_xor(a, 16, 64), __shfl_xor(b, 16, 64));
-  if (r.group_top == 2 && b > kMasked) a = ordered(number(a) + number(b));
+  if (r.group_top == 2 && b > -INFINITY) a += b;
   int before = 0;
   for (int o = 0; o < r.groups; ++o) {
-    const K x = of_lane(a, o << r.shift);
+    const F x = of_lane(a, o << r.shift);
     before += x > a || (x == a && o < g);
   }
   return g < r.groups && before < r.top_groups;
@@ -242,6 +245,7 @@ struct Held<32, K> : Searched<32, K> {
 template <int V, bool BIAS>
 __global__ __launch_bounds__(256) void moe_route_kernel(Router r) {
   using K = std::conditional_t<BIAS, uint64_t, uint32_t>;
+  using F = std::conditional_t<BIAS, double, float>;
   extern __shared__ double smem[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = blockIdx.x * r.waves + wave;
@@ -290,19 +294,21 @@ __global__ __launch_bounds__(256) void moe_route_kernel(Router r) {
       share = sum > 0.0 ? reciprocal(sum) : 0.0;
     }
   }
+  F v[V];
   K key[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if constexpr (BIAS) key[i] = ordered(p[i] * share + (double)bias[i]);
-    else key[i] = ordered(x[i]);
-    if (x[i] == -INFINITY) key[i] = lane * V + i < r.E ? kMasked : kGone;
+    if constexpr (BIAS) v[i] = x[i] == -INFINITY ? (F)x[i] : p[i] * share + (double)bias[i];
+    else v[i] = x[i];
+    key[i] = ordered(v[i]);                  // of minus infinity: a mask, below every number's
+    if (lane * V + i >= r.E) key[i] = kGone;
   }
 
   if (r.groups > 1) {
-    K* mine = reinterpret_cast<K*>(smem) + wave * r.E;
+    F* mine = reinterpret_cast<F*>(smem) + wave * r.E;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (lane * V + i < r.E) mine[lane * V + i] = key[i];
+      if (lane * V + i < r.E) mine[lane * V + i] = v[i];
     // a wave's LDS operations are done in their order; the compiler has to keep it
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
