@@ -237,3 +237,30 @@ def test_refused_on_the_gpu():
         rf.rfp2_rms_norm(x.half(), 4, 1, 64, g, EPS, x)
     with pytest.raises(rf.Rfp2Error):
         rf.rfp2_rms_norm(x[:1].expand(4, 64), 4, 1, 64, g, EPS, x)            # rows on top of each other
+
+
+def test_tensors_of_other_shapes():
+    """What holds the call's values in another shape, or more of them, is taken as before:
+    weights flat, outputs longer than the call."""
+    announce("norm, other shapes")
+    T, k, K = 3, 2, 64
+    rng, x, gain = stream_inputs(T, K, 6)
+    r, w = rng.standard_normal((T, k, K)).astype(np.float32), rng.random((T, k)).astype(np.float32)
+    h, h2 = empty((T, K), torch.float32), empty((T + 2, K), torch.float32)
+    q, d = empty((T, K), torch.int8), empty((T, K // 32), torch.float32)
+    q2, d2 = empty((T + 1, K // 4, 4), torch.int8), empty((64,), torch.float32)
+    rf.rfp2_moe_combine(to_dev(x), to_dev(r), to_dev(w), T, k, K, h, to_dev(gain), EPS, None, q, d)
+    rf.rfp2_moe_combine(to_dev(x).view(T, 2, K // 2), to_dev(r).view(-1), to_dev(w).view(-1), T, k, K, h2,
+                        to_dev(np.concatenate([gain, gain])), EPS, None, q2, d2)
+    assert torch.equal(h, h2[:T]) and torch.equal(q.view(-1), q2.view(-1)[:T * K])
+    assert torch.equal(d.view(-1), d2[:T * K // 32])
+    with pytest.raises(ValueError):
+        rf.rfp2_moe_combine(to_dev(x), to_dev(r), to_dev(w), T, k, K, h, to_dev(gain)[:32], EPS, None, q, d)
+    with pytest.raises(ValueError):
+        rf.rfp2_moe_combine(to_dev(x), to_dev(r).transpose(0, 1), to_dev(w), T, k, K, h)
+    with pytest.raises(TypeError):
+        rf.rfp2_moe_combine(to_dev(x), to_dev(r), to_dev(w).double(), T, k, K, h)
+    with pytest.raises(TypeError):
+        rf.rfp2_moe_combine(to_dev(x), r, to_dev(w), T, k, K, h)
+    with pytest.raises(ValueError):
+        rf.rfp2_moe_combine(to_dev(x), to_dev(r), torch.from_numpy(w), T, k, K, h)
