@@ -171,12 +171,12 @@ __device__ __forceinline__ bool group_stays(const F* v, const Router& r) {
 
 // A lane's V keys: its largest, where it was among the V (the first of equals), and how to
 // take it away.  Up to eight are sorted once and move up (by neighbours' exchanges, which leave
-// equals in their order); more are looked through each time.
+// equals in their order); more are lists of eight.
 template <int V, class K>
 struct Held {
   K key[V];
   int at[V];
-  __device__ __forceinline__ explicit Held(const K (&k)[V]) {
+  __device__ __forceinline__ explicit Held(const K* k) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       key[i] = k[i];
@@ -205,41 +205,33 @@ struct Held {
     }
   }
 };
-template <int V, class K>
-struct Searched {
-  K key[V], top;
-  int at;
-  __device__ __forceinline__ explicit Searched(const K (&k)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = k[i];
-    look();
+template <int N, class K>
+struct Lists {
+  Held<8, K> list;
+  Lists<N - 1, K> rest;
+  __device__ __forceinline__ explicit Lists(const K* k) : list(k), rest(k + 8) {}
+  __device__ __forceinline__ bool later() const { return rest.best() > list.best(); }
+  __device__ __forceinline__ K best() const { return later() ? rest.best() : list.best(); }
+  __device__ __forceinline__ int place() const {
+    return later() ? 8 + rest.place() : list.place();
   }
-  __device__ __forceinline__ void look() {
-    top = key[0];
-    at = 0;
-#pragma unroll
-    for (int i = 1; i < V; ++i)
-      if (key[i] > top) {
-        top = key[i];
-        at = i;
-      }
-  }
-  __device__ __forceinline__ K best() const { return top; }
-  __device__ __forceinline__ int place() const { return at; }
   __device__ __forceinline__ void take(bool mine) {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (mine && i == at) key[i] = kGone;
-    look();
+    const bool l = later();
+    list.take(mine && !l);
+    rest.take(mine && l);
   }
 };
 template <class K>
-struct Held<16, K> : Searched<16, K> {
-  using Searched<16, K>::Searched;
+struct Lists<1, K> : Held<8, K> {
+  using Held<8, K>::Held;
 };
 template <class K>
-struct Held<32, K> : Searched<32, K> {
-  using Searched<32, K>::Searched;
+struct Held<16, K> : Lists<2, K> {
+  using Lists<2, K>::Lists;
+};
+template <class K>
+struct Held<32, K> : Lists<4, K> {
+  using Lists<4, K>::Lists;
 };
 
 template <int V, bool BIAS>
