@@ -114,3 +114,31 @@ def test_values_of_all_codes():
     with np.errstate(invalid="ignore"):
         want = (q.reshape(2, 4, 32).astype(np.float32) * d[..., None]).reshape(2, 128)
     assert np.array_equal(host(out), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_codes_of_any_values(seed):
+    """Codes and scales without divisions are those of rfp2_quantize_acts bit for bit: 64 as the gate
+    passes 64 times the other half exactly (exp(-64) is below half a step of fp64), whose values
+    here have any exponent, subnormal scales and quotients close to the border of two codes among
+    them."""
+    announce("codes of any values", seed)
+    rng = np.random.default_rng(seed)
+    M, K = 1024, 4096
+    u = (rng.integers(0, 1 << 23, (M, K), dtype=np.uint32) | np.uint32(127 << 23)).view(np.float32) - 1
+    u = u * np.exp2(rng.integers(-150, 121, (M, K // 32, 1)).astype(np.float64)).repeat(32, -1).reshape(M, K)
+    u *= np.exp2(-rng.integers(0, 12, (M, K)).astype(np.float64)) * rng.choice([-1.0, 1.0], (M, K))
+    # every second row: multiples of a half of the block's scale, and their neighbours in fp32
+    b = u[::2].reshape(-1, K // 32, 32).astype(np.float32)
+    top = np.abs(b).max(-1, keepdims=True)
+    d = np.where(top > 0, (top.astype(np.float64) / 127).astype(np.float32), np.float32(1))
+    half = ((rng.integers(-127, 127, b.shape) + 0.5) * d.astype(np.float64)).astype(np.float32)
+    half = np.where(rng.random(b.shape) < 0.5, half, np.nextafter(half, np.float32(0)))
+    half[..., :1] = top
+    u = u.astype(np.float32)
+    u[::2] = half.reshape(-1, K)
+    y = to_dev(u) * 64.0
+    q, d = run(torch.full((M, K), 64.0, device=device()), to_dev(u), rf.GATE_SILU, M, K)
+    q2, d2 = empty((M, K), torch.int8), empty((M, K // 32), torch.float32)
+    rf.rfp2_quantize_acts(y, M, K, q2, d2)
+    assert np.array_equal(d, host(d2), equal_nan=True) and np.array_equal(q, host(q2))
