@@ -35,7 +35,8 @@ __device__ __forceinline__ double reciprocal(double d) {
 }
 
 // Code and scale as quantize_acts_kernel computes them, of N (4 or 8) values of
-// each of the 32 / N neighbouring lanes of a block.  Magnitudes are compared as integers, where infinities and NaN are the largest.
+// each of the 32 / N neighbouring lanes of a block.  Magnitudes are compared as integers,
+// where infinities and NaN are the largest.
 //
 // The two divisions are fp64 products with a reciprocal, rounded to fp32: the same bits as
 // a division of fp32 numbers.  A quotient X 2^a / (D 2^b) of 24-bit whole numbers is no

@@ -12,9 +12,9 @@
 // function of a smaller one is below 2^-868 and leaves nothing of any product in fp32, and
 // that of a larger one is 1.
 //
-// 4096 rows of 1536 take 11.2 us (5.1 TB/s); reading and writing their 57 MB takes 8.8, and
-// the vector instructions, some 39 a value, 7: they hide under the transfer only in part.
-// With the library's exp and divisions, 49 a value, it was 14.6 us.
+// 4096 rows of 1536 take 10.7 to 11.6 us (5.1 TB/s); reading and writing their 57 MB takes
+// 8.8, and the vector instructions, 41 a value, 7: they hide under the transfer only in
+// part.  With the library's exp and divisions it was 14.9 us.
 #include "acts_device.h"
 #include "rfp2_internal.h"
 #include "scores_device.h"

@@ -7,18 +7,16 @@
 //   w = scale * p, divided by the chosen p's sum where asked.
 //
 // Scores and choices are fp64: which of two experts is larger may hang on the last bit
-// of fp32 scores (of 4099 tokens over 256 experts with a bias, some do).  A logit of minus
-// infinity masks its expert.
+// of fp32 scores.  A logit of minus infinity masks its expert.
 //
-// One wave a token.  Lane i holds experts i V .. i V + V - 1 and the best of those that are
-// left; a choice is a maximum over the wave and the lowest lane that holds it, which is
-// the lowest expert, and only that lane's best changes.  No sort, no LDS but for groups, whose
-// experts lie across lanes.  What is chosen without a bias needs no scores: logits are compared
-// as whole numbers, and only the chosen ones' exponentials are taken (all of them where a
-// softmax is not divided by the chosen ones' sum).  What bounds it is that chain of choices and the
-// launch for few tokens (1 over 128 experts 2.7 us, 1024 over 64 2.9), the vector
-// instructions for many (4099 over 256 with a bias 7.4 us, with groups 9.8: reading the logits
-// takes 0.7).
+// One wave a token.  Lane i holds experts i V .. i V + V - 1, sorted once; a choice is a
+// maximum over the wave and the lowest lane that holds it, which is the lowest expert, and
+// that lane's list moves up.  No LDS but for groups, whose experts lie across lanes.  What
+// is chosen without a bias needs no scores: logits are compared as whole numbers, and only
+// the chosen ones' exponentials are taken (all of them where a softmax is not divided by the
+// chosen ones' sum).  What bounds it is the chain of choices and the launch for few tokens
+// (1 over 128 experts 2.6 us, 1024 over 64 2.7), the vector instructions for many (4099
+// over 256 with a bias 7.4 us, with groups 9.4: reading the logits takes 0.7).
 #include <cmath>
 #include <type_traits>
 

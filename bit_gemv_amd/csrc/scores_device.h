@@ -12,8 +12,8 @@ constexpr double kLog2E = 1.4426950408889634074;
 constexpr double kRound = 6755399441055744.0;   // 1.5 * 2^52: a sum with it ends at the units
 
 // 2^(n + f) for whole n, |n| <= 1000, handed over as m = n + kRound (its low word is n), and
-// |f| <= 1/2 or little more, within 2^-45 of it: 2^f by the polynomial of degree 9 that meets it at the
-// ten Chebyshev points of [-1/2, 1/2], n added to the exponent.
+// |f| <= 1/2 or little more, within 2^-45 of it: 2^f by the polynomial of degree 9 that
+// meets it at the ten Chebyshev points of [-1/2, 1/2], n added to the exponent.
 __device__ __forceinline__ double exp2_parts(double m, double f) {
   double p = 1.0205905413765595e-07;
   p = fma(p, f, 1.325964524488711e-06);
