@@ -199,11 +199,14 @@ struct RowChoice {
 
 // As many threads as a row has quads to give each of them two or three (one row of 4096: 3.2
 // us with 512 threads or 1024, 4.0 with 256; 4096 rows of 5120: 51.0 us with 512, 53.0 with
-// 256, 53.9 with 320, 68 with 128; 4096 rows of 2048: 18.4 with 512, 43.6 with one wave).
+// 256, 53.9 with 320, 68 with 128; 4096 rows of 2048: 18.4 with 512, 43.6 with one wave;
+// 8000 rows of 256: 6.1 with one wave, 6.8 with 128, 9.0 with 256).
 // What is longer than 16384 values stays out of the registers (one row of 32768: 11.2 us;
 // 17.0 with eight quads a thread).
 template <int MODE, int PAST>
 RowChoice choose_row(int64_t quads) {
+  if (quads <= 64) return {row_norm_kernel<MODE, 64, 1, PAST>, 64};
+  if (quads <= 128) return {row_norm_kernel<MODE, 128, 1, PAST>, 128};
   if (quads <= 256) return {row_norm_kernel<MODE, 256, 1, PAST>, 256};
   if (quads <= 512) return {row_norm_kernel<MODE, 512, 1, PAST>, 512};
   if (quads <= 1024) return {row_norm_kernel<MODE, 512, 2, PAST>, 512};

@@ -169,3 +169,43 @@ def test_rows_past_the_caches(K, values):
     rf.rfp2_moe_combine(y2, rows[at], w[at], 4, 1, K, h2, gain, EPS, xs)
     rf.rfp2_moe_combine(x, rows, w, T, 1, K, x, gain, EPS, y)           # onto the stream in place
     assert torch.equal(x[at], h2) and torch.equal(y[at], xs)
+
+
+def rounded(y, ref):
+    """Half a step of fp32 and of its smallest numbers, and the fp64 arithmetic."""
+    return bool(((y.double() - ref).abs() <= (2.0 ** -24 + 2.0 ** -43) * ref.abs() + 2.0 ** -150).all())
+
+
+def test_the_widest_rows():
+    announce("rows of 2^24 values")
+    K = 1 << 24
+    x, a, gain = normal(1, K), normal(1, K, seed=2), normal(K, seed=3)
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    q, d = torch.empty(1, K, dtype=torch.int8, device=device()), torch.empty(1, K // 32, device=device())
+    rf.rfp2_add_rms_norm(x, a, 1, K, gain, EPS, h, y, q, d)
+    assert torch.equal(h, x + a)
+    t = h.double()
+    assert rounded(y, t / torch.sqrt((t * t).mean() + EPS) * gain.double())
+    q2, d2 = torch.empty_like(q), torch.empty_like(d)
+    rf.rfp2_quantize_acts(y, 1, K, q2, d2)
+    assert torch.equal(q, q2) and torch.equal(d, d2)
+    rf.rfp2_moe_combine(x, a, torch.ones(1, 1, device=device()), 1, 1, K, h, gain, EPS, None, q2, d2)
+    assert torch.equal(h, x + a) and torch.equal(q, q2) and torch.equal(d, d2)
+    rf.rfp2_quantize_gated_acts(x, a, 1, K, rf.GATE_SILU, q, d)
+    g = x.double()
+    rf.rfp2_quantize_acts((g / (1 + torch.exp(-g)) * a.double()).float(), 1, K, q2, d2)
+    assert torch.equal(d, d2) and torch.equal(q, q2)
+    rf.rfp2_dequantize_acts(q, d, 1, K, y)
+    assert torch.equal(y, (q.view(-1, 32).float() * d.view(-1, 1)).view(1, K))
+
+
+@pytest.mark.parametrize("T,k,K", [(1, 1024, 64), (3, 1024, 4096), (1000, 1, 32)])
+def test_the_most_rows_a_token(T, k, K):
+    announce("combine of many rows", T, k, K)
+    x, rows, w, h = normal(T, K), normal(T, k, K, seed=2), normal(T, k, seed=3), torch.empty(T, K, device=device())
+    rf.rfp2_moe_combine(x, rows, w, T, k, K, h)
+    terms = w.double()[..., None] * rows.double()
+    ref = x.double() + terms.sum(1)
+    size = x.double().abs() + terms.abs().sum(1)
+    # one rounding to fp32; k + 1 terms in fp64, in any order, on either side
+    assert bool(((h.double() - ref).abs() <= 2.0 ** -24 * ref.abs() + 2 * (k + 2) * 2.0 ** -53 * size).all())

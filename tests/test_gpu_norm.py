@@ -44,7 +44,7 @@ def test_heads(T, H, D, gap):
 
 
 # rows and widths: odd counts, one value group, widths that end inside a workgroup's reach, wide ones
-ROWS = [(1, 32), (1, 4096), (3, 64), (2, 96), (5, 2048), (7, 5120), (33, 1056), (2, 16384), (1, 32768),
+ROWS = [(1, 32), (9, 256), (3, 288), (5, 512), (4, 544), (1, 4096), (3, 64), (2, 96), (5, 2048), (7, 5120), (33, 1056), (2, 16384), (1, 32768),
         (3, 34816), (2, 100000), (600, 4096), (1100, 160), (513, 8192)]
 
 
@@ -89,9 +89,9 @@ def test_add_norm(T, K):
         assert torch.equal(h3, h[:, :K]) if "h" in want else not h3.any()
         assert torch.equal(y3, y[:, :K]) if "y" in want else not y3.any()
         assert torch.equal(q3, q2) and torch.equal(d3, d2) if "q" in want else not q3.any() and not d3.any()
-    for over in ("x", "add", "both"):
+    for over in ("x", "add", "both", "swapped"):
         xs, as_ = xg.clone(), ag.clone()
-        ho, yo = (xs, None) if over == "x" else (as_, None) if over == "add" else (xs, as_)
+        ho, yo = {"x": (xs, None), "add": (as_, None), "both": (xs, as_), "swapped": (as_, xs)}[over]
         q4, d4 = torch.empty_like(q2), torch.empty_like(d2)
         rf.rfp2_add_rms_norm(xs, as_, T, K, gg, EPS, ho, yo, q4, d4)
         assert torch.equal(ho[:, :K], h[:, :K]) and torch.equal(q4, q2) and torch.equal(d4, d2), over
