@@ -11,12 +11,12 @@
 //
 // One wave a token.  Lane i holds experts i V .. i V + V - 1, sorted once; a choice is a
 // maximum over the wave and the lowest lane that holds it, which is the lowest expert, and
-// that lane's list moves up.  No LDS but for groups, whose experts lie across lanes.  What
-// is chosen without a bias needs no scores: logits are compared as whole numbers, and only
+// that lane's list moves up.  LDS holds what lies across lanes: groups, and the chosen
+// experts' scores.  What is chosen without a bias needs no scores: logits are compared as whole numbers, and only
 // the chosen ones' exponentials are taken (all of them where a softmax is not divided by the
 // chosen ones' sum).  What bounds it is the chain of choices and the launch for few tokens
-// (1 over 128 experts 2.6 us, 1024 over 64 2.7), the vector instructions for many (4099
-// over 256 with a bias 7.4 us, with groups 9.4: reading the logits takes 0.7).
+// (1 over 128 experts 2.6 us, 1024 over 64 2.5), the vector instructions for many (4099
+// over 256 with a bias 7.2 us, with groups 9.3: reading the logits takes 0.7).
 #include <cmath>
 #include <type_traits>
 
@@ -232,6 +232,12 @@ struct Held<32, K> : Lists<4, K> {
   using Lists<4, K>::Lists;
 };
 
+// A wave's LDS operations are done in their order; the compiler has to keep it.
+__device__ __forceinline__ void in_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 template <int V, bool BIAS>
 __global__ __launch_bounds__(256) void moe_route_kernel(Router r) {
   using K = std::conditional_t<BIAS, uint64_t, uint32_t>;
@@ -274,8 +280,13 @@ __global__ __launch_bounds__(256) void moe_route_kernel(Router r) {
     top = number(wave_max(m));
   }
   double p[V];
-  if (BIAS || (!r.sigmoid && !r.renorm)) {
+  const bool all = BIAS || (!r.sigmoid && !r.renorm);   // scores of all experts, kept in LDS
+  double* kept = smem + wave * r.E;
+  if (all) {
     scores<V>(p, x, top, r.sigmoid);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane * V + i < r.E) kept[lane * V + i] = p[i];
     if (!r.sigmoid) {
       double sum = 0.0;
 #pragma unroll
@@ -295,13 +306,11 @@ __global__ __launch_bounds__(256) void moe_route_kernel(Router r) {
   }
 
   if (r.groups > 1) {
-    F* mine = reinterpret_cast<F*>(smem) + wave * r.E;
+    F* mine = reinterpret_cast<F*>(smem + (all ? r.waves * r.E : 0)) + wave * r.E;
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (lane * V + i < r.E) mine[lane * V + i] = v[i];
-    // a wave's LDS operations are done in their order; the compiler has to keep it
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    in_order();
     const uint64_t stays = __ballot(group_stays(mine, r));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -320,11 +329,14 @@ __global__ __launch_bounds__(256) void moe_route_kernel(Router r) {
   }
 
   double w = 0.0;
-  if (lane < r.top_k) {
+  if (all) {
+    in_order();
+    if (lane < r.top_k) w = kept[id] * share;
+  } else if (lane < r.top_k) {
     const float mine[1] = {l[id]};
     double s[1];
     scores<1>(s, mine, top, r.sigmoid);
-    w = s[0] * share;
+    w = s[0];
   }
   if (r.renorm) {
     const double total = group_sum<64>(w);
@@ -354,7 +366,9 @@ hipError_t launch_moe_route(const float* logits, int64_t T, int64_t E, int64_t s
   const int32_t per = (int32_t)E / groups;
   // Few tokens: a wave a workgroup, more compute units for them.
   const int32_t waves = T >= 1024 && E <= 512 ? 4 : 1;
-  const size_t lds = groups > 1 ? (size_t)waves * E * sizeof(double) : 0;   // at most 16 KiB
+  // at most 32 KiB: scores, and what groups are compared by
+  const int tables = (bias || (!sigmoid && !renorm)) + (groups > 1);
+  const size_t lds = (size_t)tables * waves * E * sizeof(double);
   for (int64_t t = 0; t < T; t += kMaxGrid) {
     const Router r = {logits + t * stride, bias, ids + t * top_k, weights + t * top_k, err, scale,
                       stride, (int32_t)std::min(T - t, kMaxGrid), (int32_t)E, groups, group_top,

@@ -39,7 +39,7 @@ def gated(g, u, gelu):
     # 0.5 (1 + tanh z) is written as 1 / (1 + exp(-2 z)): the same number, but for z < 0 the
     # sum 1 + tanh z cancels (at z = -18 nothing is left of it in 53 bits)
     z = 2.0 * math.sqrt(2.0 / math.pi) * (g + 0.044715 * g ** 3) if gelu else g
-    with np.errstate(over="ignore"):
+    with np.errstate(over="ignore", invalid="ignore"):     # an infinite gate gives NaN
         return g / (1.0 + np.exp(-z)) * u
 
 
