@@ -8,7 +8,7 @@
 // code, and so the codes are those of the definition whatever the order of the sums.
 // Everything here is bound by the transfer, a value read once and written once: 4096 rows
 // of 5120 added, normed and quantized take 47 us (275 MB, 5.9 TB/s), 512 tokens of eight
-// experts' rows of 4096 15 us (86 MB, 5.7 TB/s); a single row 2.9 us, of which the launch
+// experts' rows of 4096 15 us (86 MB, 5.7 TB/s); a single row 2.6 us, of which the launch
 // is 1.7.
 #include "acts_device.h"
 #include "rfp2_internal.h"
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const float* x, int 
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int e = 0; e < 4; ++e) s = fma((double)v[c][e], (double)v[c][e], s);
-  const double inv = 1.0 / sqrt(group_sum<G>(s) / D + eps);
+  const double inv = inverse_root(fma(group_sum<G>(s), reciprocal((double)D), eps));
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = 4 * (lane + c * G);
@@ -129,6 +129,7 @@ __global__ __launch_bounds__(THREADS) void row_norm_kernel(NormRows r) {
   __shared__ double part[THREADS / 64];
   const int64_t t = blockIdx.x;
   const int quads = r.K >> 2;
+  const double inv_k = reciprocal((double)r.K);
   float v[C][4], g[C][4];
   double s = 0.0;
 #pragma unroll
@@ -158,15 +159,13 @@ __global__ __launch_bounds__(THREADS) void row_norm_kernel(NormRows r) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) s = fma((double)x[e], (double)x[e], s);
   }
-  s = group_sum<64>(s);
-  if (THREADS > 64) {
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
-    __syncthreads();
-    s = part[0];
+  s = sum_in_last_lane(s);
+  if ((threadIdx.x & 63) == 63) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = part[0];
 #pragma unroll
-    for (int w = 1; w < THREADS / 64; ++w) s += part[w];
-  }
-  const double inv = 1.0 / sqrt(s / (double)r.K + r.eps);
+  for (int w = 1; w < THREADS / 64; ++w) s += part[w];
+  const double inv = inverse_root(fma(s, inv_k, r.eps));
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = threadIdx.x + c * THREADS;
@@ -264,8 +263,8 @@ template <int G, int C>
 hipError_t launch_heads(const float* x, int64_t T, int64_t H, int64_t D, int64_t x_stride,
                         const float* gain, double eps, float* y, int64_t y_stride,
                         hipStream_t stream) {
-  // One head a group of lanes: 2049 rows of 40 heads of 128 take 14.2 us (5.9 TB/s) and 14.7
-  // with four, one row 2.0 and 2.9.  Large outputs go past the caches (16.9 us without, at 64
+  // One head a group of lanes: 2049 rows of 40 heads of 128 take 13.2 us (6.4 TB/s; 14.2 before
+  // the root was shortened, and 14.7 with four heads), one row 2.0 and 2.9.  Large outputs go past the caches (16.9 us without, at 64
   // rows no difference).
   const auto kernel =
       T * H * D >= (1 << 20) ? rms_norm_kernel<G, C, true> : rms_norm_kernel<G, C, false>;

@@ -30,7 +30,7 @@ __device__ __forceinline__ double exp2_parts(double m, double f) {
   return __builtin_bit_cast(double, b + ((uint64_t)(n << 20) << 32));
 }
 
-// 1 / (1 + 2^(n + f)) within 2^-42 of it.
+// 1 / (1 + 2^(n + f)) within 2^-44 of it.
 __device__ __forceinline__ double logistic_parts(double m, double f) {
   const double d = 1.0 + exp2_parts(m, f);
   const double r = __builtin_amdgcn_rcp(d);
