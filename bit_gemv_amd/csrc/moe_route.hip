@@ -14,9 +14,10 @@
 // that lane's list moves up.  LDS holds what lies across lanes: groups, and the chosen
 // experts' scores.  What is chosen without a bias needs no scores: logits are compared as
 // whole numbers, and only the chosen ones' exponentials are taken (all of them where a
-// softmax is not divided by the chosen ones' sum).  What bounds it is the chain of choices and the launch for few tokens
-// (1 over 128 experts 2.6 us, 1024 over 64 2.5), the vector instructions for many (4099
-// over 256 with a bias 7.2 us, with groups 9.3: reading the logits takes 0.7).
+// softmax is not divided by the chosen ones' sum).  What bounds it is the chain of choices
+// and the launch for few tokens (1 over 128 experts 2.6 us, 1024 over 64 2.5), the vector
+// instructions for many (4099 over 256 with a bias 7.2 us, with groups 9.3: reading the
+// logits takes 0.7).
 #include <cmath>
 #include <type_traits>
 

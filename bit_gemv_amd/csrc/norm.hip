@@ -263,9 +263,9 @@ template <int G, int C>
 hipError_t launch_heads(const float* x, int64_t T, int64_t H, int64_t D, int64_t x_stride,
                         const float* gain, double eps, float* y, int64_t y_stride,
                         hipStream_t stream) {
-  // One head a group of lanes: 2049 rows of 40 heads of 128 take 13.2 us (6.4 TB/s; 14.2 before
-  // the root was shortened, and 14.7 with four heads), one row 2.0 and 2.9.  Large outputs go past the caches (16.9 us without, at 64
-  // rows no difference).
+  // One head a group of lanes: 2049 rows of 40 heads of 128 take 13.2 us (6.4 TB/s; 14.2
+  // before the root was shortened, and 14.7 with four heads), one row 2.0 and 2.9.  Large
+  // outputs go past the caches (16.9 us without, at 64 rows no difference).
   const auto kernel =
       T * H * D >= (1 << 20) ? rms_norm_kernel<G, C, true> : rms_norm_kernel<G, C, false>;
   const int64_t per = kThreads / G, parts = std::min<int64_t>((H + per - 1) / per, 65535);
