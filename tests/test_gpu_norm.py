@@ -96,6 +96,10 @@ def test_add_norm(T, K):
         rf.rfp2_add_rms_norm(xs, as_, T, K, gg, EPS, ho, yo, q4, d4)
         assert torch.equal(ho[:, :K], h[:, :K]) and torch.equal(q4, q2) and torch.equal(d4, d2), over
         assert yo is None or torch.equal(yo[:, :K], y[:, :K])
+    for over in (0, 1):                                            # y over a source, no stream
+        rows = [xg.clone(), ag.clone()]
+        rf.rfp2_add_rms_norm(*rows, T, K, gg, EPS, None, rows[over])
+        assert torch.equal(rows[over][:, :K], y[:, :K])
 
 
 @pytest.mark.parametrize("T,K", [(1, 32), (4, 4096), (3, 33024), (520, 2048)])
@@ -157,6 +161,9 @@ def test_combine(T, k, K):
     assert torch.equal(h3, h[:, :K])
     rf.rfp2_moe_combine(xg, rg, wg, T, k, K, None, gg, EPS, None, q3, d3)
     assert torch.equal(q3, q) and torch.equal(d3, d)
+    over = rows_apart(x, 12)
+    rf.rfp2_moe_combine(over, rg, wg, T, k, K, over)
+    assert torch.equal(over[:, :K], h[:, :K])
     rf.rfp2_moe_combine(None, rg, wg, T, k, K, h3)
     assert_rounded(host(h3), ff.combine(None, r, w), size)
     rf.rfp2_moe_combine(xg, rg, wg, T, k, K, xg, gg, EPS, None, q3, d3)
