@@ -340,7 +340,17 @@ __global__ __launch_bounds__(256) void moe_route_kernel(Router r) {
     w = s[0];
   }
   if (r.renorm) {
-    const double total = group_sum<64>(w);
+    double total = group_sum<64>(w);
+    // Scores so small that some of them count as 0 (e^-346; those are below e^-690): the
+    // exponentials over the largest chosen one's, since there a sigmoid's 1 / (1 + e^l) is 1 within
+    // 2^-499 and a softmax's sum is the same for all.
+    if (of_lane(total, 0) < 0x1p-500) {      // the wave's lanes together
+      const float mine[1] = {lane < r.top_k ? l[id] : -INFINITY};
+      double s[1];
+      scores<1>(s, mine, number(wave_max(ordered(mine[0]))), false);
+      w = s[0];
+      total = group_sum<64>(w);
+    }
     w = total > 0.0 ? w * reciprocal(total) : 0.0;
   }
   if (lane < r.top_k) {

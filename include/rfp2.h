@@ -566,10 +566,11 @@ rfp2_status rfp2_moe_combine(const float* x, const float* rows, const float* wei
  *   top_groups best groups stay.  The top_k largest v among what stays are
  *   chosen, in falling order; among equal groups or experts the lower comes
  *   first.  v and p are fp64 (a sigmoid's logit, or one less the token's largest
- *   in a softmax, below -690 makes p 0).
+ *   in a softmax, below -690 makes p 0; renorm goes by the chosen logits there, and
+ *   its weights are the formula's however small the scores are).
  *   ids     [T][top_k] int32, 4-byte aligned.
  *   weights [T][top_k] fp32, 4-byte aligned: scale * p of the chosen, where
- *          renorm != 0 divided by the sum of the chosen p (0 where that is 0).
+ *          renorm != 0 divided by the sum of the chosen p (0 where all are masked).
  *   err     nullable device int32: a token with a logit of NaN or plus infinity,
  *          or any bias that is not finite, gets ids of -1 and weights of NaN, and
  *          1 is written to *err (never cleared by the call).

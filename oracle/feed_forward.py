@@ -55,6 +55,18 @@ def scores(logits, sigmoid):
     return [x / total if total else 0.0 for x in e]
 
 
+def shares(logits, p):
+    """The chosen experts' scores p over their sum; 0 where all are masked.  Of scores so small
+    that fp64 loses some, the exponentials over the largest one's: there a sigmoid's 1 / (1 + e^l)
+    is 1 within 2^-499, and a softmax's sum is the same for all."""
+    total = math.fsum(p)
+    if total < 2.0 ** -500:
+        top = max(logits)
+        p = [0.0 if l == -math.inf else math.exp(float(l) - float(top)) for l in logits]
+        total = math.fsum(p)
+    return [x / total if total else 0.0 for x in p]
+
+
 def route(logits, bias, sigmoid, groups, group_top, top_groups, top_k, renorm, scale):
     """One token -> (ids, fp64 weights)."""
     E = len(logits)
@@ -71,6 +83,5 @@ def route(logits, bias, sigmoid, groups, group_top, top_groups, top_k, renorm, s
     ids = sorted(there, key=lambda e: (-v[e], e))[:top_k]
     w = [p[e] for e in ids]
     if renorm:
-        total = math.fsum(w)
-        w = [x / total if total else 0.0 for x in w]
+        w = shares([logits[e] for e in ids], w)
     return ids, [scale * x for x in w]
