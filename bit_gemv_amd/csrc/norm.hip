@@ -256,15 +256,22 @@ template <int MODE>
 hipError_t launch_rows(const NormRows& r, int64_t T, hipStream_t stream) {
   const int64_t quads = r.K / 4;
   // More than an XCD's 4 MB second-level cache of output goes past the caches (512 rows of 4096:
-  // 6.7 us so, 7.6 without; 300: 5.0 and 5.4; 150: 3.6 and 3.7).  Rows of 64 MB and more
-  // are read past them as well (4096 rows of 5120: 46.7 us so, 51.0 without; 2000 of 4096: 20.9
-  // and 18.2, where they are still in the last-level cache); the experts' rows never.
+  // 6.4 us so, 7.2 without; 256: 3.5 and 3.8; 128: 3.2 and 3.3).  Two rows to be added, of 64 MB
+  // and more each, are read past them as well (4096 rows of 5120: 46.5 us so, 50.7 without; 3000:
+  // 35.8 and 38.5; 2048 rows of 4096: 20.5 and 18.0); a row alone only where it is read twice (600
+  // of 32768: 36.8 and 39.9; but 4096 of 4096 19.5 and 16.3, 4096 of 5120 23.1 and 22.9, 8192
+  // 43.1 and 43.5); the experts' rows never.
   const int64_t values = T * r.K;
-  RowChoice c;
-  if (values < (1 << 20)) c = choose_row<MODE, KEEP>(quads);
-  else if (MODE == MODE_SUM || values < (1 << 24)) c = choose_row<MODE, STREAM_OUT>(quads);
-  else c = choose_row<MODE, MODE == MODE_SUM ? STREAM_OUT : STREAM_ALL>(quads);
   const bool sum_alone = MODE == MODE_SUM && !r.gain;
+  RowChoice c = {};
+  if (!sum_alone) {
+    if (values < (1 << 20)) c = choose_row<MODE, KEEP>(quads);
+    else if (MODE == MODE_SUM || values < (1 << 24)) c = choose_row<MODE, STREAM_OUT>(quads);
+    else if constexpr (MODE == MODE_ADD) c = choose_row<MODE, STREAM_ALL>(quads);
+    else if constexpr (MODE == MODE_ROW)
+      c = quads <= kMostQuads ? choose_row<MODE, STREAM_OUT>(quads)
+                              : RowChoice{row_norm_kernel<MODE, 1024, 4, STREAM_ALL>, 1024};
+  }
   const int64_t parts = sum_alone ? (quads + kThreads - 1) / kThreads : 1;
   for (int64_t t = 0; t < T; t += kMaxGrid / parts) {
     const int64_t n = std::min(T - t, kMaxGrid / parts);
