@@ -131,7 +131,10 @@ hipError_t launch_quantize_gated_acts(const float* gate, const float* up, int64_
 
 hipError_t launch_dequantize_acts(const int8_t* q, const float* d, int64_t M, int64_t K, float* a,
                                   hipStream_t stream) {
-  // Large outputs go past the caches: 4096 rows of 5120 22.6 us without, 16.8 so (6.4 TB/s).
+  // From 2^23 values on (32 MB, the XCDs' second-level caches together) the output goes past the
+  // caches: 4096 rows of 5120 16.8 us so (6.4 TB/s), 22.5 without; 2048 of 4096 7.0 and 8.1; 1024
+  // 4.1 and 5.1.  A kernel that reads all of it at once pays for that (with one that scales the
+  // values 51.3 and 46.0, 20.2 and 18.4, 11.8 and 11.7), so that smaller ones stay.
   const int64_t quads = M * (K / 4), per = 4 * kThreads, most = per * kMaxGrid;
   const auto kernel =
       quads >= (1 << 21) ? dequantize_acts_kernel<true> : dequantize_acts_kernel<false>;

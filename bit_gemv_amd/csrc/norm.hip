@@ -201,7 +201,10 @@ __global__ __launch_bounds__(THREADS) void row_norm_kernel(NormRows r) {
   }
 }
 
-// The weighted sum alone: quads [blockIdx.y * 256, ...) of a row.
+// The weighted sum alone: quads [blockIdx.y * 256, ...) of a row.  Stores are ordinary at any
+// size, since the stream is read next: 2000 rows of 4096 from one expert each take 15.4 us past
+// the caches and 16.9 so, but with the norm that reads them 41.7 and 38.1; 512 from eight 13.3
+// either way, 21.4 and 21.5 with the norm.
 __global__ __launch_bounds__(kThreads) void combine_kernel(NormRows r) {
   const int64_t t = blockIdx.x;
   const int i = blockIdx.y * kThreads + threadIdx.x;
@@ -217,12 +220,15 @@ struct RowChoice {
   int threads;
 };
 
-// As many threads as a row has quads to give each of them two or three (one row of 4096: 3.2
-// us with 512 threads or 1024, 4.0 with 256; 4096 rows of 5120: 51.0 us with 512, 53.0 with
-// 256, 53.9 with 320, 68 with 128; 4096 rows of 2048: 18.4 with 512, 43.6 with one wave;
-// 8000 rows of 256: 6.1 with one wave, 6.8 with 128, 9.0 with 256).
-// What is longer than 16384 values stays out of the registers (one row of 32768: 11.2 us;
-// 17.0 with eight quads a thread).
+// One quad a thread up to 512 threads, then up to three, beyond 6144 values 1024 threads with up
+// to four.  One row, in us, with the threads x quads taken here first: 512 values 1.9 with 128x1,
+// 2.3 with 64x2; 1024 1.9 with 256x1, 2.4 with 128x2; 2048 2.2 with 512x1, 2.3 with 1024x1, 2.5
+// with 256x2; 4096 2.7 with 512x2, 2.8 with 1024x1, 3.6 with 256x4; 5120 3.0 with 512x3 or
+// 1024x2; 6144 3.4 with 512x3, 3.3 with 1024x2; 8192 3.9 with 1024x2, 4.1 with 512x4.  1024 rows,
+// sums of eight experts: 4096 32.4 with 512x2, 34.1 with 1024x1; 6144 48.9 with 512x3, 50.6 with
+// 1024x2 (fewer rows of such sums: 128 of 4096 6.2 and 6.0, 16 4.0 with either).  8000 rows of
+// 256 6.1 with one wave, 9.0 with 256 threads.  What is longer than 16384 values stays out of the
+// registers (one row of 32768: 10.8; 17.0 with eight quads a thread).
 template <int MODE, int PAST>
 RowChoice choose_row(int64_t quads) {
   if (quads <= 64) return {row_norm_kernel<MODE, 64, 1, PAST>, 64};
