@@ -490,9 +490,13 @@ rfp2_status rfp2_paged_attn(const rfp2_kv_cache* cache, const float* q, int64_t 
  * weighted sum back onto the stream.  fp32 rows come in; what a product takes
  * next goes out (int8 activations exactly as rfp2_quantize_acts gives them
  * for the fp32 values, expert ids).  Inner arithmetic is fp64 with one
- * rounding to fp32, so that codes and choices are those of the definition;
- * infinities and NaN go through the formulas (a block of 32 that holds one
- * gets d = NaN, q = 0).
+ * rounding to fp32: a value is the fp32 number next to the formula's, or the
+ * other neighbour where the formula's lies within the fp64 error of their
+ * middle, and codes and scales are the quantizer's of these.  That error is at
+ * most 2^-43 of a value or of the sum of its terms' magnitudes (2^-40 in rows of
+ * more than 16384 values, whose squares a thread adds by the hundreds and more;
+ * 2^-41 where a gelu is below 2^-149 of its gate).  Infinities and NaN go through
+ * the formulas (a block of 32 that holds one gets d = NaN, q = 0).
  *
  * rfp2_rms_norm -- the norm of each head (of a query or key before rfp2_rope):
  *   y = x * gain / sqrt(mean over the head of x^2 + eps).
@@ -565,9 +569,11 @@ rfp2_status rfp2_moe_combine(const float* x, const float* rows, const float* wei
  *   group_top (1 or 2) largest v (by those that are not masked), and only the
  *   top_groups best groups stay.  The top_k largest v among what stays are
  *   chosen, in falling order; among equal groups or experts the lower comes
- *   first.  v and p are fp64 (a sigmoid's logit, or one less the token's largest
- *   in a softmax, below -690 makes p 0; renorm goes by the chosen logits there, and
- *   its weights are the formula's however small the scores are).
+ *   first.  v and p are fp64, p within 2^-43 of the formula's: with a bias, scores
+ *   that differ by less may come in either order (those of equal logits and biases
+ *   are equal).  A sigmoid's logit, or one less the token's largest in a softmax,
+ *   below -690 makes p 0; renorm goes by the chosen logits there, and its weights
+ *   are the formula's however small the scores are.
  *   ids     [T][top_k] int32, 4-byte aligned.
  *   weights [T][top_k] fp32, 4-byte aligned: scale * p of the chosen, where
  *          renorm != 0 divided by the sum of the chosen p (0 where all are masked).
