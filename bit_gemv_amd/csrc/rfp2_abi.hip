@@ -17,6 +17,12 @@ bool aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
+// Whether n bytes at p and m bytes at q share any (both far below 2^63).
+bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b ? b - a < (uintptr_t)n : a - b < (uintptr_t)m;
+}
+
 rfp2_status from_hip(hipError_t e) {
   return e == hipSuccess ? RFP2_OK : RFP2_E_LAUNCH;
 }
@@ -474,6 +480,8 @@ rfp2_status rfp2_dequantize_acts(const int8_t* q, const float* d, int64_t M, int
   if (M < 1 || M > kMaxRows || K < 32 || K % 32 != 0 || K > (int64_t(1) << 30))
     return RFP2_E_SHAPE;
   if (!aligned(q, 4) || !aligned(d, 4) || !aligned(a, 16)) return RFP2_E_ALIGN;
+  if (overlap(a, 4 * M * K, q, M * K) || overlap(a, 4 * M * K, d, M * (K / 8)))
+    return RFP2_E_SHAPE;
   (void)hipGetLastError();
   return from_hip(rfp2::launch_dequantize_acts(q, d, M, K, a, stream));
 }

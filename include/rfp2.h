@@ -617,7 +617,7 @@ rfp2_status rfp2_quantize_gated_acts(const float* gate, const float* up, int64_t
  * a = fl32(q * d): the reverse of rfp2_quantize_acts (a router or any other
  * reader of fp32 values can follow a call that wrote q and d alone).
  *   q, d as rfp2_quantize_acts writes them, 4-byte aligned; a [M][K] fp32,
- *   16-byte aligned.
+ *   16-byte aligned, no overlap with q or d (refused: others still read them).
  * Requires M >= 1, K >= 32, K % 32 == 0, K <= 2^30.
  */
 rfp2_status rfp2_dequantize_acts(const int8_t* q, const float* d, int64_t M, int64_t K, float* a,
